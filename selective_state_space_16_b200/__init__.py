@@ -21,3 +21,14 @@ from .binding import (  # noqa: F401
     ssm_workspace_init,
     status_string,
 )
+from .gated import (  # noqa: F401
+    gated_scan_bwd,
+    gated_scan_fwd,
+    new_gated_checkpoints,
+    new_gated_workspace,
+    ssm_gated_bwd_workspace_size,
+    ssm_gated_checkpoint_size,
+    ssm_gated_scan_bwd,
+    ssm_gated_scan_fwd,
+    ssm_gated_state_update,
+)

@@ -1,0 +1,223 @@
+// gated_api.cu -- the C ABI of the gated linear recurrence (ssm_gated.h): argument checks,
+// workspace layout, dispatch over the element type.
+#include <cmath>
+#include <limits>
+
+#include "gated_host.h"
+#include "host_common.h"
+
+namespace {
+
+using namespace ssmh;
+using ssm::GatedParams;
+using ssm::GatedTensor;
+
+// Sums over the batch rows, in their order: dlam, dr_bias and di_bias of a channel.
+__global__ void __launch_bounds__(128) gated_bwd_params_kernel(const float* part, const float* lam, float* dlam, float* drb,
+                                                               float* dib, int batch, int dim) {
+    const int d = blockIdx.x * 128 + threadIdx.x;
+    if (d >= dim) return;
+    const long long rows = static_cast<long long>(batch) * dim;
+    float s[3] = {0.f, 0.f, 0.f};
+    for (int b = 0; b < batch; ++b)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) s[k] += part[k * rows + static_cast<long long>(b) * dim + d];
+    if (dlam) {  // T is dL / d log v: sigmoid / softplus -> 1 for lam -> -inf
+        const float l = lam[d], e = expf(l);
+        dlam[d] = s[0] * (l < -15.f ? 1.f : l > 20.f ? 1.f / l : e / (1.f + e) / log1pf(e));
+    }
+    if (drb) drb[d] = s[1];
+    if (dib) dib[d] = s[2];
+}
+
+bool valid_sizes(int batch, int dim, int64_t seqlen) { return batch >= 0 && dim >= 0 && seqlen >= 0; }
+
+bool supported_sizes(int batch, int dim, int64_t seqlen) {
+    return static_cast<long long>(batch) * dim < (1LL << 31) && seqlen < (1LL << 31) - 1024;
+}
+
+// Floats of a row of checkpoints: one for each group of steps, of which the first can begin up to
+// 15 steps before the row (an aligned window), rounded up to 16 bytes.
+long long checkpoint_row(int64_t seqlen) {
+    return static_cast<long long>(round_up((static_cast<size_t>(seqlen) + 15 + ssm::kGroup - 1) / ssm::kGroup, 4));
+}
+
+GatedTensor tensor(const ssm_gated_in_t& t) { return {t.data, t.batch_stride, t.dim_stride}; }
+GatedTensor tensor(const ssm_gated_out_t& t) { return {t.data, t.batch_stride, t.dim_stride}; }
+
+bool element_aligned(const void* p, int io) {
+    return (reinterpret_cast<uintptr_t>(p) & (io == SSM_BF16 ? 1u : 3u)) == 0;
+}
+bool float_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks what forward and backward read alike and fills the kernels' parameters.
+ssm_status_t common_params(const ssm_gated_args_t* a, GatedParams* p) {
+    if (!a || !valid_sizes(a->batch, a->dim, a->seqlen)) return SSM_ERR_INVALID_ARG;
+    if (a->io_dtype != SSM_F32 && a->io_dtype != SSM_BF16) return SSM_ERR_INVALID_ARG;
+    if (!(a->c > 0.f) || !std::isfinite(a->c)) return SSM_ERR_INVALID_ARG;
+    if (!supported_sizes(a->batch, a->dim, a->seqlen)) return SSM_ERR_UNSUPPORTED;
+    const bool rows = a->batch > 0 && a->dim > 0;
+    if (rows && !a->lam) return SSM_ERR_INVALID_ARG;
+    if (rows && a->seqlen > 0 && (!a->x.data || !a->r.data || !a->i.data)) return SSM_ERR_INVALID_ARG;
+    for (const void* q : {a->x.data, a->r.data, a->i.data, a->z.data})
+        if (!element_aligned(q, a->io_dtype)) return SSM_ERR_INVALID_ARG;
+    for (const void* q : {static_cast<const void*>(a->lam), static_cast<const void*>(a->r_bias), static_cast<const void*>(a->i_bias),
+                          static_cast<const void*>(a->initial_state), static_cast<const void*>(a->lengths)})
+        if (!float_aligned(q)) return SSM_ERR_INVALID_ARG;
+    *p = GatedParams{};
+    p->x = tensor(a->x);
+    p->r = tensor(a->r);
+    p->i = tensor(a->i);
+    p->z = tensor(a->z);
+    p->lam = a->lam;
+    p->r_bias = a->r_bias;
+    p->i_bias = a->i_bias;
+    p->h0 = a->initial_state;
+    p->lengths = a->lengths;
+    p->reset = a->reset;
+    p->batch = a->batch;
+    p->dim = a->dim;
+    p->L = static_cast<int>(a->seqlen);
+    p->ckpt_row = checkpoint_row(a->seqlen);
+    p->c = a->c;
+    return SSM_OK;
+}
+
+// Whether no two rows of an output overlap (channels inside batch rows, or the other way round).
+bool rows_apart(const GatedTensor& t, int batch, int dim, int64_t L) {
+    const auto nested = [L](long long n_out, long long s_out, long long n_in, long long s_in) {
+        const long long inner = n_in > 1 ? (s_in >= L ? (n_in - 1) * s_in + L : -1) : L;
+        return inner >= 0 && (n_out <= 1 || s_out >= inner);
+    };
+    return nested(batch, t.bs, dim, t.ds) || nested(dim, t.ds, batch, t.bs);
+}
+
+bool is_input(const ssm_gated_args_t* a, const void* q) {
+    return q && (q == a->x.data || q == a->r.data || q == a->i.data || q == a->z.data);
+}
+
+ssm_status_t launch_fwd(int io, const GatedParams& p, cudaStream_t s) {
+    return io == SSM_BF16 ? launch_gated_fwd<__nv_bfloat16>(p, s) : launch_gated_fwd<float>(p, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssm_gated_checkpoint_size(int batch, int dim, int64_t seqlen) {
+    if (!valid_sizes(batch, dim, seqlen) || !supported_sizes(batch, dim, seqlen)) return 0;
+    return static_cast<size_t>(batch) * dim * checkpoint_row(seqlen) * sizeof(float);
+}
+
+ssm_status_t ssm_gated_scan_fwd(const ssm_gated_args_t* args, ssm_gated_out_t y, float* last_state, void* checkpoints,
+                                ssm_stream_t stream) {
+    GatedParams p;
+    ssm_status_t st = common_params(args, &p);
+    if (st != SSM_OK) return st;
+    const bool rows = p.batch > 0 && p.dim > 0;
+    if (rows && p.L > 0 && !y.data) return SSM_ERR_INVALID_ARG;
+    if (is_input(args, y.data) || !element_aligned(y.data, args->io_dtype)) return SSM_ERR_INVALID_ARG;
+    if (!float_aligned(last_state) || !aligned16(checkpoints)) return SSM_ERR_INVALID_ARG;
+    p.y = tensor(y);
+    if (rows && p.L > 0 && !rows_apart(p.y, p.batch, p.dim, p.L)) return SSM_ERR_INVALID_ARG;
+    if (!rows) return SSM_OK;
+    st = check_device(nullptr);
+    if (st != SSM_OK) return st;
+    p.last = last_state;
+    p.ckpt = static_cast<float*>(checkpoints);
+    return launch_fwd(args->io_dtype, p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t ssm_gated_bwd_workspace_size(int batch, int dim, int64_t seqlen, int have_checkpoints) {
+    if (!valid_sizes(batch, dim, seqlen) || !supported_sizes(batch, dim, seqlen)) return 0;
+    const size_t sums = round_up(static_cast<size_t>(batch) * dim * 3 * sizeof(float), 256);
+    return sums + (have_checkpoints ? 0 : round_up(ssm_gated_checkpoint_size(batch, dim, seqlen), 256));
+}
+
+ssm_status_t ssm_gated_scan_bwd(const ssm_gated_args_t* args, const ssm_gated_grads_t* grads, const void* checkpoints,
+                                void* workspace, size_t workspace_bytes, ssm_stream_t stream) {
+    GatedParams p;
+    ssm_status_t st = common_params(args, &p);
+    if (st != SSM_OK) return st;
+    if (!grads) return SSM_ERR_INVALID_ARG;
+    const ssm_gated_grads_t& g = *grads;
+    const bool rows = p.batch > 0 && p.dim > 0;
+    if (rows && p.L > 0 && (!g.dy.data || !g.dx.data || !g.dr.data || !g.di.data || (args->z.data && !g.dz.data)))
+        return SSM_ERR_INVALID_ARG;
+    for (const void* q : {g.dx.data, g.dr.data, g.di.data, g.dz.data})
+        if (is_input(args, q) || (q && q == g.dy.data) || !element_aligned(q, args->io_dtype)) return SSM_ERR_INVALID_ARG;
+    if (!element_aligned(g.dy.data, args->io_dtype) || !aligned16(checkpoints)) return SSM_ERR_INVALID_ARG;
+    for (const void* q : {static_cast<const void*>(g.dlast_state), static_cast<const void*>(g.dlam), static_cast<const void*>(g.dr_bias),
+                          static_cast<const void*>(g.di_bias), static_cast<const void*>(g.dinitial_state)})
+        if (!float_aligned(q)) return SSM_ERR_INVALID_ARG;
+    p.dy = tensor(g.dy);
+    p.dx = tensor(g.dx);
+    p.dr = tensor(g.dr);
+    p.di = tensor(g.di);
+    p.dz = tensor(g.dz);
+    if (rows && p.L > 0)
+        for (const GatedTensor* t : {&p.dx, &p.dr, &p.di, p.z.p ? &p.dz : &p.dx})
+            if (!rows_apart(*t, p.batch, p.dim, p.L)) return SSM_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool sums = g.dlam || g.dr_bias || g.di_bias;
+    if (p.dim == 0) return SSM_OK;
+    if (p.batch == 0 || p.L == 0) {  // no steps: the sums are zero, the state's gradient passes through
+        st = check_device(nullptr);
+        if (st != SSM_OK) return st;
+        cudaError_t e = cudaSuccess;
+        for (float* q : {g.dlam, g.dr_bias, g.di_bias})
+            if (q && e == cudaSuccess) e = cudaMemsetAsync(q, 0, static_cast<size_t>(p.dim) * sizeof(float), s);
+        const size_t bytes = static_cast<size_t>(p.batch) * p.dim * sizeof(float);
+        if (g.dinitial_state && bytes && e == cudaSuccess)
+            e = g.dlast_state ? cudaMemcpyAsync(g.dinitial_state, g.dlast_state, bytes, cudaMemcpyDeviceToDevice, s)
+                              : cudaMemsetAsync(g.dinitial_state, 0, bytes, s);
+        return e == cudaSuccess ? SSM_OK : SSM_ERR_LAUNCH;
+    }
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+        workspace_bytes < ssm_gated_bwd_workspace_size(p.batch, p.dim, p.L, checkpoints != nullptr))
+        return SSM_ERR_WORKSPACE;
+    st = check_device(nullptr);
+    if (st != SSM_OK) return st;
+    p.dlast = g.dlast_state;
+    p.part = sums ? static_cast<float*>(workspace) : nullptr;
+    p.ckpt = static_cast<float*>(const_cast<void*>(checkpoints));
+    if (!checkpoints) {
+        p.ckpt = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                          round_up(static_cast<size_t>(p.batch) * p.dim * 3 * sizeof(float), 256));
+        GatedParams f = p;  // a forward that stores nothing but the checkpoints
+        f.z.p = nullptr;
+        st = launch_fwd(args->io_dtype, f, s);
+        if (st != SSM_OK) return st;
+    }
+    p.dh0 = g.dinitial_state;
+    st = args->io_dtype == SSM_BF16 ? launch_gated_bwd<__nv_bfloat16>(p, s) : launch_gated_bwd<float>(p, s);
+    if (st != SSM_OK || !sums) return st;
+    gated_bwd_params_kernel<<<static_cast<unsigned>((p.dim + 127) / 128), 128, 0, s>>>(p.part, p.lam, g.dlam, g.dr_bias,
+                                                                                       g.di_bias, p.batch, p.dim);
+    return launch_status();
+}
+
+ssm_status_t ssm_gated_state_update(const ssm_gated_step_t* args, ssm_stream_t stream) {
+    if (!args) return SSM_ERR_INVALID_ARG;
+    const ssm_gated_step_t& a = *args;
+    if (a.batch < 0 || a.dim < 0 || a.n_slots < 0) return SSM_ERR_INVALID_ARG;
+    if (a.io_dtype != SSM_F32 && a.io_dtype != SSM_BF16) return SSM_ERR_INVALID_ARG;
+    if (!(a.c > 0.f) || !std::isfinite(a.c)) return SSM_ERR_INVALID_ARG;
+    if (a.batch == 0 || a.dim == 0) return SSM_OK;
+    if (!a.x || !a.r || !a.i || !a.y || !a.lam || (a.n_slots > 0 && !a.state)) return SSM_ERR_INVALID_ARG;
+    if (a.state_stride < a.dim && a.n_slots > 1) return SSM_ERR_INVALID_ARG;
+    if (a.batch > 1 && (a.y_stride < a.dim)) return SSM_ERR_INVALID_ARG;
+    if (a.y == a.x || a.y == a.r || a.y == a.i || a.y == a.z) return SSM_ERR_INVALID_ARG;
+    for (const void* q : {a.x, a.r, a.i, a.z, static_cast<const void*>(a.y)})
+        if (!element_aligned(q, a.io_dtype)) return SSM_ERR_INVALID_ARG;
+    for (const void* q : {static_cast<const void*>(a.state), static_cast<const void*>(a.slots), static_cast<const void*>(a.lam),
+                          static_cast<const void*>(a.r_bias), static_cast<const void*>(a.i_bias)})
+        if (!float_aligned(q)) return SSM_ERR_INVALID_ARG;
+    if (a.batch > 65535) return SSM_ERR_UNSUPPORTED;  // the batch row is a grid y index
+    const ssm_status_t st = check_device(nullptr);
+    if (st != SSM_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return a.io_dtype == SSM_BF16 ? launch_gated_step<__nv_bfloat16>(a, s) : launch_gated_step<float>(a, s);
+}
+
+}  // extern "C"

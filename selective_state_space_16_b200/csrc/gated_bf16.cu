@@ -1,0 +1,8 @@
+// gated_bf16.cu -- the gated linear recurrence for bf16 elements (gated_launch.cuh).
+#include "gated_launch.cuh"
+
+namespace ssmh {
+template ssm_status_t launch_gated_fwd<__nv_bfloat16>(const ssm::GatedParams&, cudaStream_t);
+template ssm_status_t launch_gated_bwd<__nv_bfloat16>(const ssm::GatedParams&, cudaStream_t);
+template ssm_status_t launch_gated_step<__nv_bfloat16>(const ssm_gated_step_t&, cudaStream_t);
+}  // namespace ssmh

@@ -1,0 +1,261 @@
+"""ctypes binding of the gated linear recurrence (include/ssm_gated.h).
+
+Argument marshalling only, as in binding.py: the argument structs are packed with struct (one call
+instead of a ctypes object per field, which is most of the host time of a one-token step).  Calls
+go to the tensors' own device, on its current stream unless another stream is given.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import struct
+
+import torch
+
+from . import binding
+from .binding import SSM_BF16, SSM_F32, _check
+
+# The layouts of ssm_gated_args_t, ssm_gated_grads_t, ssm_gated_step_t and ssm_gated_out_t.
+_ARGS = struct.Struct("@Pqq Pqq Pqq Pqq PPP PPP q iiif")
+_GRADS = struct.Struct("@Pqq P Pqq Pqq Pqq Pqq PPPP")
+_STEP = struct.Struct("@Pq P PPPP P qqqqq PPP iiiif 4x")
+
+
+class GatedOut(ctypes.Structure):
+    """ssm_gated_out_t: a (batch, dim, seqlen) output."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("dim_stride", ctypes.c_int64)]
+
+
+def declare(lib: ctypes.CDLL) -> None:
+    """Declare the argument and result types of this header's entry points."""
+    vp, ci, i64, sz, st = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_char_p
+    lib.ssm_gated_checkpoint_size.argtypes = [ci, ci, i64]
+    lib.ssm_gated_checkpoint_size.restype = sz
+    lib.ssm_gated_bwd_workspace_size.argtypes = [ci, ci, i64, ci]
+    lib.ssm_gated_bwd_workspace_size.restype = sz
+    lib.ssm_gated_scan_fwd.argtypes = [st, GatedOut, vp, vp, vp]
+    lib.ssm_gated_scan_fwd.restype = ci
+    lib.ssm_gated_scan_bwd.argtypes = [st, st, vp, vp, sz, vp]
+    lib.ssm_gated_scan_bwd.restype = ci
+    lib.ssm_gated_state_update.argtypes = [st, vp]
+    lib.ssm_gated_state_update.restype = ci
+
+
+_IO = {torch.bfloat16: SSM_BF16, torch.float32: SSM_F32}
+
+
+def _call(tensor, stream, fn, *args):
+    """fn(*args, stream) with the tensor's device current."""
+    dev = tensor.device
+    if stream is not None:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    else:
+        raw = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        return fn(*args, raw)
+    with torch.cuda.device(dev):
+        return fn(*args, raw)
+
+
+@contextlib.contextmanager
+def _allocating(tensor, stream):
+    """Allocations inside belong to the tensor's device and to the stream that the call runs on, so that
+    torch neither hands out memory still in use on it nor reuses theirs before it is done."""
+    if not tensor.is_cuda:
+        raise ValueError("x: not a CUDA tensor")
+    with torch.cuda.device(tensor.device):
+        if stream is None:
+            yield
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=tensor.device)
+        with torch.cuda.stream(stream):
+            yield
+
+
+def _dense(t, name, shape, dtypes, dev):
+    """Address of an optional dense tensor."""
+    if t is None:
+        return 0
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype} (expected {' or '.join(str(d) for d in dtypes)})")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a dense tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    return t.data_ptr()
+
+
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_FLAG = (torch.uint8, torch.bool)
+
+
+def _seq(t, name, like):
+    """Address, batch stride and dim stride of a (batch, dim, seqlen) operand."""
+    if t is None:
+        return 0, 0, 0
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name}: {t.dtype} (x is {like.dtype})")
+    if t.shape != like.shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} (x has {tuple(like.shape)})")
+    sb, sd, sl = t.stride()
+    if sl != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: consecutive steps must be next to each other (stride {sl})")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, x on {like.device}")
+    return t.data_ptr(), sb, sd
+
+
+def _args(x, r, i, lam, r_bias, i_bias, z, initial_state, lengths, reset, c):
+    io = _IO.get(x.dtype)
+    if io is None:
+        raise TypeError(f"unsupported I/O dtype {x.dtype}")
+    if x.dim() != 3:
+        raise ValueError(f"x: expected (batch, dim, seqlen), got {tuple(x.shape)}")
+    if not x.is_cuda:
+        raise ValueError("x: not a CUDA tensor")
+    b, d, L = x.shape
+    dev = x.device
+    if lam is None:
+        raise ValueError("lam is required")
+    ch, rows = (d,), (b, d)
+    return _ARGS.pack(*_seq(x, "x", x), *_seq(r, "r", x), *_seq(i, "i", x), *_seq(z, "z", x),
+                      _dense(lam, "lam", ch, _F32, dev), _dense(r_bias, "r_bias", ch, _F32, dev),
+                      _dense(i_bias, "i_bias", ch, _F32, dev), _dense(initial_state, "initial_state", rows, _F32, dev),
+                      _dense(lengths, "lengths", (b,), _I32, dev), _dense(reset, "reset", (b, L), _FLAG, dev), L, b, d, io, c)
+
+
+def _buffer(t, name, bytes_, dev):
+    if t is None:
+        return 0
+    if not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name}: expected a dense tensor on {dev}")
+    if t.numel() * t.element_size() < bytes_:
+        raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes, {bytes_} needed")
+    return t.data_ptr()
+
+
+def ssm_gated_checkpoint_size(batch: int, dim: int, seqlen: int) -> int:
+    return int(binding.load().ssm_gated_checkpoint_size(batch, dim, seqlen))
+
+
+def ssm_gated_bwd_workspace_size(batch: int, dim: int, seqlen: int, have_checkpoints: bool = False) -> int:
+    return int(binding.load().ssm_gated_bwd_workspace_size(batch, dim, seqlen, int(bool(have_checkpoints))))
+
+
+def new_gated_checkpoints(batch, dim, seqlen, device="cuda"):
+    """Allocate (with torch) the checkpoints that a forward call stores for its backward."""
+    return torch.empty(ssm_gated_checkpoint_size(batch, dim, seqlen), dtype=torch.uint8, device=device)
+
+
+def new_gated_workspace(batch, dim, seqlen, have_checkpoints=False, device="cuda"):
+    """Allocate (with torch) a workspace of the backward for these sizes."""
+    return torch.empty(max(ssm_gated_bwd_workspace_size(batch, dim, seqlen, have_checkpoints), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def ssm_gated_scan_fwd(x, r, i, lam, r_bias, i_bias, z, y, last_state, initial_state=None, lengths=None, reset=None,
+                       checkpoints=None, c=8.0, stream=None, check=True):
+    """Marshal a forward call.  x/r/i/z/y: (b, d, L), any batch and channel strides; lam/r_bias/i_bias: (d)
+    fp32 (biases may be None); z may be None; last_state/initial_state: (b, d) fp32 or None; lengths: (b)
+    int32 or None; reset: (b, L) uint8 or bool or None; checkpoints: from new_gated_checkpoints, or None."""
+    args = _args(x, r, i, lam, r_bias, i_bias, z, initial_state, lengths, reset, c)
+    b, d, L = x.shape
+    dev = x.device
+    ck = 0 if checkpoints is None else _buffer(checkpoints, "checkpoints", ssm_gated_checkpoint_size(b, d, L), dev)
+    code = _call(x, stream, binding.load().ssm_gated_scan_fwd, args, GatedOut(*_seq(y, "y", x)),
+                 _dense(last_state, "last_state", (b, d), _F32, dev), ck)
+    if check:
+        _check(code, "ssm_gated_scan_fwd")
+    return code
+
+
+def ssm_gated_scan_bwd(x, r, i, lam, r_bias, i_bias, z, dy, dx, dr, di, dlam, dr_bias, di_bias, dz, workspace,
+                       initial_state=None, dlast_state=None, dinitial_state=None, lengths=None, reset=None,
+                       checkpoints=None, c=8.0, stream=None, check=True):
+    """Marshal a backward call (shapes as the forward; dlam/dr_bias/di_bias (d) fp32 or None, dinitial_state
+    (b, d) fp32 or None; dz required with z; checkpoints: the forward's, or None)."""
+    args = _args(x, r, i, lam, r_bias, i_bias, z, initial_state, lengths, reset, c)
+    b, d, L = x.shape
+    dev, ch, rows = x.device, (d,), (b, d)
+    grads = _GRADS.pack(*_seq(dy, "dy", x), _dense(dlast_state, "dlast_state", rows, _F32, dev), *_seq(dx, "dx", x),
+                        *_seq(dr, "dr", x), *_seq(di, "di", x), *_seq(dz, "dz", x), _dense(dlam, "dlam", ch, _F32, dev),
+                        _dense(dr_bias, "dr_bias", ch, _F32, dev), _dense(di_bias, "di_bias", ch, _F32, dev),
+                        _dense(dinitial_state, "dinitial_state", rows, _F32, dev))
+    ck = 0 if checkpoints is None else _buffer(checkpoints, "checkpoints", ssm_gated_checkpoint_size(b, d, L), dev)
+    code = _call(x, stream, binding.load().ssm_gated_scan_bwd, args, grads, ck, _buffer(workspace, "workspace", 0, dev),
+                 0 if workspace is None else workspace.numel() * workspace.element_size())
+    if check:
+        _check(code, "ssm_gated_scan_bwd")
+    return code
+
+
+def ssm_gated_state_update(state, x, r, i, lam, r_bias, i_bias, z, y, slots=None, c=8.0, stream=None, check=True):
+    """Marshal a one-token step.  state: (slots, d) fp32 in/out, rows of any stride; x/r/i/z/y: (b, d), rows of
+    any stride; slots: (b) int32, the state of each row (outside the pool: the row is skipped), or None."""
+    io = _IO.get(x.dtype)
+    if io is None:
+        raise TypeError(f"unsupported I/O dtype {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError("x: not a CUDA tensor")
+    b, d = x.shape
+    dev = x.device
+    at = []
+    for name, t in (("x", x), ("r", r), ("i", i), ("z", z), ("y", y)):
+        if t is None and name == "z":
+            at.append((0, 0))
+            continue
+        if t.dtype != x.dtype or t.shape != x.shape or t.device != dev:
+            raise ValueError(f"{name}: expected {tuple(x.shape)} {x.dtype} on {dev}")
+        rs, cs = t.stride()
+        if cs != 1 and d > 1:
+            raise ValueError(f"{name}: channels must be next to each other (stride {cs})")
+        at.append((t.data_ptr(), rs))
+    if lam is None:
+        raise ValueError("lam is required")
+    if state.dtype != torch.float32 or state.dim() != 2 or state.shape[1] != d or state.device != dev:
+        raise ValueError(f"state: expected (slots, {d}) torch.float32 on {dev}")
+    ss, cs = state.stride()
+    if cs != 1 and d > 1:
+        raise ValueError(f"state: channels must be next to each other (stride {cs})")
+    (xp, xs), (rp, rs), (ip, is_), (zp, zs), (yp, ys) = at
+    ch = (d,)
+    args = _STEP.pack(state.data_ptr(), ss, _dense(slots, "slots", (b,), _I32, dev), xp, rp, ip, zp, yp, xs, rs, is_, zs, ys,
+                      _dense(lam, "lam", ch, _F32, dev), _dense(r_bias, "r_bias", ch, _F32, dev),
+                      _dense(i_bias, "i_bias", ch, _F32, dev), b, d, state.shape[0], io, c)
+    code = _call(x, stream, binding.load().ssm_gated_state_update, args)
+    if check:
+        _check(code, "ssm_gated_state_update")
+    return code
+
+
+def gated_scan_fwd(x, r, i, lam, r_bias=None, i_bias=None, z=None, initial_state=None, lengths=None, reset=None,
+                   return_last_state=True, checkpoints=None, c=8.0, stream=None):
+    """Convenience wrapper: allocates y (x's dtype; zeros behind the rows' lengths) and last_state (fp32) and
+    calls ssm_gated_scan_fwd.  Returns (y, last_state)."""
+    with _allocating(x, stream):
+        y = (torch.empty if lengths is None else torch.zeros)(x.shape, dtype=x.dtype, device=x.device)
+        last = torch.empty(x.shape[:2], dtype=torch.float32, device=x.device) if return_last_state else None
+        ssm_gated_scan_fwd(x, r, i, lam, r_bias, i_bias, z, y, last, initial_state=initial_state, lengths=lengths, reset=reset,
+                           checkpoints=checkpoints, c=c, stream=stream)
+    return y, last
+
+
+def gated_scan_bwd(x, r, i, lam, r_bias=None, i_bias=None, z=None, dy=None, initial_state=None, dlast_state=None,
+                   lengths=None, reset=None, checkpoints=None, workspace=None, c=8.0, stream=None):
+    """Convenience wrapper: allocates every gradient and, if not given, a workspace, then calls
+    ssm_gated_scan_bwd.  Returns a dict dx, dr, di, dz (or None), dlam, dr_bias, di_bias, dinitial_state."""
+    b, d, L = x.shape
+    f32 = dict(dtype=torch.float32, device=x.device)
+    with _allocating(x, stream):
+        out = {k: torch.empty(x.shape, dtype=x.dtype, device=x.device) for k in ("dx", "dr", "di")}
+        out["dz"] = None if z is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out.update({k: torch.empty(d, **f32) for k in ("dlam", "dr_bias", "di_bias")}, dinitial_state=torch.empty((b, d), **f32))
+        if workspace is None:
+            workspace = new_gated_workspace(b, d, L, checkpoints is not None, device=x.device)
+        ssm_gated_scan_bwd(x, r, i, lam, r_bias, i_bias, z, dy, out["dx"], out["dr"], out["di"], out["dlam"], out["dr_bias"],
+                           out["di_bias"], out["dz"], workspace, initial_state=initial_state, dlast_state=dlast_state,
+                           dinitial_state=out["dinitial_state"], lengths=lengths, reset=reset, checkpoints=checkpoints, c=c,
+                           stream=stream)
+    return out
