@@ -32,3 +32,12 @@ from .gated import (  # noqa: F401
     ssm_gated_scan_fwd,
     ssm_gated_state_update,
 )
+from .cache import (  # noqa: F401
+    CachePools,
+    new_cache_workspace,
+    ssm_cache_compact,
+    ssm_cache_copy,
+    ssm_cache_fork,
+    ssm_cache_free,
+    ssm_cache_workspace_size,
+)

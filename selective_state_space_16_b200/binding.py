@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI in include/ssm_scan.h (gated.py: include/ssm_gated.h).
+"""ctypes binding of the C ABI in include/ssm_scan.h (gated.py: include/ssm_gated.h,
+cache.py: include/ssm_cache.h).
 
 Argument marshalling only: every step of the scan runs in the CUDA kernels of
 libssm_scan.so.  Tensors are torch tensors used purely as device memory; the
@@ -99,8 +100,9 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.ssm_selective_scan_fwd_conv.restype = ci
     lib.ssm_read_status.argtypes = [vp, vp]
     lib.ssm_read_status.restype = ci
-    from . import gated
+    from . import cache, gated
     gated.declare(lib)
+    cache.declare(lib)
     return lib
 
 
