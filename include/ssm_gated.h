@@ -30,7 +30,7 @@
  *     SSM_ERR_INVALID_ARG); it must not overlap another
  *     argument; initial_state and last_state of the forward may be the same buffer.
  *   - Every sum is formed in a fixed order: repeated calls give identical results.
- *   - batch * dim < 2^31, seqlen < 2^31 - 1024 (SSM_ERR_UNSUPPORTED).
+ *   - batch * dim < 2^31, seqlen < 2^31 - 65536 (SSM_ERR_UNSUPPORTED).
  */
 #ifndef SSM_GATED_H
 #define SSM_GATED_H

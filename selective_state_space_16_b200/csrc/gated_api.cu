@@ -33,13 +33,13 @@ __global__ void __launch_bounds__(128) gated_bwd_params_kernel(const float* part
 bool valid_sizes(int batch, int dim, int64_t seqlen) { return batch >= 0 && dim >= 0 && seqlen >= 0; }
 
 bool supported_sizes(int batch, int dim, int64_t seqlen) {
-    return static_cast<long long>(batch) * dim < (1LL << 31) && seqlen < (1LL << 31) - 1024;
+    return static_cast<long long>(batch) * dim < (1LL << 31) && seqlen < (1LL << 31) - (1 << 16);  // (steps are 32-bit in the kernels)
 }
 
 // Floats of a row of checkpoints: one for each group of steps, of which the first can begin up to
-// 15 steps before the row (an aligned window), rounded up to 16 bytes.
+// kGroup - 1 steps before the row (an aligned window), rounded up to 16 bytes.
 long long checkpoint_row(int64_t seqlen) {
-    return static_cast<long long>(round_up((static_cast<size_t>(seqlen) + 15 + ssm::kGroup - 1) / ssm::kGroup, 4));
+    return static_cast<long long>(round_up((static_cast<size_t>(seqlen) + 2 * (ssm::kGroup - 1)) / ssm::kGroup, 4));
 }
 
 GatedTensor tensor(const ssm_gated_in_t& t) { return {t.data, t.batch_stride, t.dim_stride}; }
@@ -106,7 +106,7 @@ extern "C" {
 
 size_t ssm_gated_checkpoint_size(int batch, int dim, int64_t seqlen) {
     if (!valid_sizes(batch, dim, seqlen) || !supported_sizes(batch, dim, seqlen)) return 0;
-    return static_cast<size_t>(batch) * dim * checkpoint_row(seqlen) * sizeof(float);
+    return sizeof(ssm::CkptHeader) + static_cast<size_t>(batch) * dim * checkpoint_row(seqlen) * sizeof(float);
 }
 
 ssm_status_t ssm_gated_scan_fwd(const ssm_gated_args_t* args, ssm_gated_out_t y, float* last_state, void* checkpoints,

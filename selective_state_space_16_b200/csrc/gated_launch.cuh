@@ -8,30 +8,71 @@
 
 namespace ssmh {
 
+// How rows are laid on lanes.  Short rows share a warp (2 or 8 lanes of 8 steps each); few long rows are
+// split over the warps of a block until the GPU has work for all its SMs.
+struct GatedShape {
+    int seg, split;
+};
+
+inline GatedShape gated_shape(long long rows, int L) {
+    if (L <= 2 * ssm::kGroup) return {2, 1};
+    if (L <= 8 * ssm::kGroup) return {8, 1};
+    int split = 1;
+    while (split < ssm::kMaxSplit && rows * split < 148 * 16 && split * ssm::kTile < L) split *= 2;
+    return {32, split};
+}
+
+using GatedKernel = void (*)(const ssm::GatedParams);
+
+template <typename IO, bool GATE, bool RESET>
+GatedKernel gated_kernel(GatedShape shape, bool backward) {
+    if (shape.seg == 2) return backward ? ssm::gated_bwd_kernel<IO, GATE, RESET, 2, false> : ssm::gated_fwd_kernel<IO, GATE, RESET, 2, false>;
+    if (shape.seg == 8) return backward ? ssm::gated_bwd_kernel<IO, GATE, RESET, 8, false> : ssm::gated_fwd_kernel<IO, GATE, RESET, 8, false>;
+    if (shape.split > 1) return backward ? ssm::gated_bwd_kernel<IO, GATE, RESET, 32, true> : ssm::gated_fwd_kernel<IO, GATE, RESET, 32, true>;
+    return backward ? ssm::gated_bwd_kernel<IO, GATE, RESET, 32, false> : ssm::gated_fwd_kernel<IO, GATE, RESET, 32, false>;
+}
+
+template <typename IO>
+ssm_status_t launch_gated(ssm::GatedParams p, bool backward, cudaStream_t stream) {
+    const long long rows = static_cast<long long>(p.batch) * p.dim;
+    const GatedShape shape = gated_shape(rows, p.L);
+    p.split = shape.split;
+    const bool gate = p.z.p != nullptr, reset = p.reset != nullptr;
+    const GatedKernel kern = gate ? (reset ? gated_kernel<IO, true, true>(shape, backward) : gated_kernel<IO, true, false>(shape, backward))
+                                  : (reset ? gated_kernel<IO, false, true>(shape, backward) : gated_kernel<IO, false, false>(shape, backward));
+    const int block = shape.split > 1 ? shape.split * 32 : ssm::kGatedWarps * 32;
+    const long long per_block = shape.split > 1 ? 1 : block / shape.seg;
+    kern<<<static_cast<unsigned>((rows + per_block - 1) / per_block), block, 0, stream>>>(p);
+    return launch_status();
+}
+
 template <typename IO>
 ssm_status_t launch_gated_fwd(const ssm::GatedParams& p, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(p.batch) * p.dim;
-    const bool gate = p.z.p != nullptr, reset = p.reset != nullptr;
-    auto kern = gate ? (reset ? ssm::gated_fwd_kernel<IO, true, true> : ssm::gated_fwd_kernel<IO, true, false>)
-                     : (reset ? ssm::gated_fwd_kernel<IO, false, true> : ssm::gated_fwd_kernel<IO, false, false>);
-    kern<<<static_cast<unsigned>((rows + ssm::kGatedWarps - 1) / ssm::kGatedWarps), ssm::kGatedWarps * 32, 0, stream>>>(p);
-    return launch_status();
+    return launch_gated<IO>(p, false, stream);
 }
 
 template <typename IO>
 ssm_status_t launch_gated_bwd(const ssm::GatedParams& p, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(p.batch) * p.dim;
-    const bool gate = p.z.p != nullptr, reset = p.reset != nullptr;
-    auto kern = gate ? (reset ? ssm::gated_bwd_kernel<IO, true, true> : ssm::gated_bwd_kernel<IO, true, false>)
-                     : (reset ? ssm::gated_bwd_kernel<IO, false, true> : ssm::gated_bwd_kernel<IO, false, false>);
-    kern<<<static_cast<unsigned>((rows + ssm::kGatedWarps - 1) / ssm::kGatedWarps), ssm::kGatedWarps * 32, 0, stream>>>(p);
-    return launch_status();
+    return launch_gated<IO>(p, true, stream);
 }
 
 template <typename IO>
 ssm_status_t launch_gated_step(const ssm_gated_step_t& a, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>((a.dim + ssm::kStepThreads - 1) / ssm::kStepThreads), static_cast<unsigned>(a.batch));
-    ssm::gated_step_kernel<IO><<<grid, ssm::kStepThreads, 0, stream>>>(a);
+    const unsigned mask = ssm::kStepChannels * sizeof(IO) - 1;
+    const auto on = [](const void* p, long long stride, unsigned m) {
+        return ((reinterpret_cast<uintptr_t>(p) | static_cast<unsigned long long>(stride)) & m) == 0;
+    };
+    const auto io = [&](const void* p, long long stride) { return on(p, stride * static_cast<long long>(sizeof(IO)), mask); };
+    const bool vec = io(a.x, a.x_stride) && io(a.r, a.r_stride) && io(a.i, a.i_stride) && io(a.z, a.z ? a.z_stride : 0) &&
+                     io(a.y, a.y_stride) && on(a.state, a.state_stride * 4, 15) && on(a.lam, 0, 15) && on(a.r_bias, 0, 15) &&
+                     on(a.i_bias, 0, 15);
+    const int per_block = ssm::kStepThreads * ssm::kStepChannels;
+    const dim3 grid(static_cast<unsigned>((a.dim + per_block - 1) / per_block), static_cast<unsigned>(a.batch));
+    const ssm::GatedStep g{a, vec};
+    if (a.z)
+        ssm::gated_step_kernel<IO, true><<<grid, ssm::kStepThreads, 0, stream>>>(g);
+    else
+        ssm::gated_step_kernel<IO, false><<<grid, ssm::kStepThreads, 0, stream>>>(g);
     return launch_status();
 }
 

@@ -23,15 +23,22 @@ struct GatedParams {
     float* last;
     const int* lengths;
     const unsigned char* reset;
-    float* ckpt;  // (rows, ckpt_row): state before every group of kGroup steps, or null
+    float* ckpt;  // CkptHeader, then (rows, ckpt_row): the state before every group of a row; or null
     int batch, dim, L;
     long long ckpt_row;
     float c;
+    int split;  // warps that share a row (1: a row per warp or part of one)
     // backward
     GatedTensor dy, dx, dr, di, dz;
     const float* dlast;
     float* dh0;
     float* part;  // (3, rows): sums of T, dr and di over a row's steps, or null
+};
+
+// Where the groups of the checkpointed rows start (phase_of their x): row (b, d) has the phase
+// (base + b * bs + d * ds) mod 16 bytes, in elements.  The backward goes by it, wherever its x is.
+struct CkptHeader {
+    unsigned base, bs, ds, pad;
 };
 
 constexpr int kGroup = 8;           // steps that a lane holds at once, and between two checkpoints
@@ -53,21 +60,41 @@ __device__ __forceinline__ float sqrt_approx(float x) {
     return y;
 }
 
-// softplus(lam), once per row and so by the library functions: large lam return lam itself.
-__device__ __forceinline__ float softplus_once(float lam) { return lam > 20.f ? lam : log1pf(expf(lam)); }
+// softplus(lam) = max(lam, 0) + log1p(e^{-|lam|}) as softplus_f32, with the exponent's product by
+// log2(e) carried to twice the length: lam reaches far below 0, where its rounding alone would cost
+// |lam| 2^-24 of the result.  About 2^-21 relative.
+__device__ __forceinline__ float softplus_lam(float lam) {
+    constexpr float c[] = SSM_LOG1P_POLY;
+    constexpr float kLog2eLow = 1.925963033500e-8f;  // log2(e) - kLog2e
+    const float x = -fabsf(lam), y = x * kLog2e;
+    const float low = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -y));
+    float e = ex2_mufu(y);
+    e = fmaf(e, low * kLn2, e);
+    float p = c[8];
+#pragma unroll
+    for (int i = 7; i >= 0; --i) p = fmaf(p, e, c[i]);
+    return fmaf(e, p, fmaxf(lam, 0.f));
+}
 
-// 1 - a^2 = 1 - e^{-u} with u = 2 v >= 0, from y = -v log2(e) and a = 2^y.  Near a = 1 the
-// difference cancels, so below u = 1/4 the series u (1 - u/2 + u^2/6 - ...) up to u^6 / 720 takes its
-// place: the first term left out is 5e-8 of the sum there, and above the border the cancellation
-// costs at most 2e-6.  For both element types: the state and the parameters' gradients are fp32.
-__device__ __forceinline__ float one_minus_square(float y, float a) {
-    const float u = y * (-2.f * kLn2);
-    float p = fmaf(u, -1.f / 720, 1.f / 120);
-    p = fmaf(u, p, -1.f / 24);
-    p = fmaf(u, p, 1.f / 6);
-    p = fmaf(u, p, -0.5f);
-    p = u * fmaf(u, p, 1.f);
-    return u < 0.25f ? p : fmaf(-a, a, 1.f);
+// The decay a = e^{-v} and 1 - a^2 = -w (2 + w), w = a - 1, from y = -v log2(e).  Near a = 1 the
+// difference w cancels, so below v = 1/8 the series w = -v (1 - v/2 + v^2/6 - ...) up to v^6 / 720
+// takes its place (the first term left out is 1e-9 of the sum there; above the border the cancellation
+// costs at most 2e-6 of w), and a = 1 + w is then good to half a step.  For both element types: the
+// state and the parameters' gradients are fp32.
+struct Decay {
+    float a, m2;  // m2 = 1 - a^2
+};
+
+__device__ __forceinline__ Decay decay_of(float y) {
+    const float e = ex2_mufu(y), x = y * kLn2;
+    float p = fmaf(x, 1.f / 720, 1.f / 120);
+    p = fmaf(x, p, 1.f / 24);
+    p = fmaf(x, p, 1.f / 6);
+    p = fmaf(x, p, 0.5f);
+    p = fmaf(x * x, p, x);
+    const bool near = x > -0.125f;
+    const float w = near ? p : e - 1.f;
+    return {near ? 1.f + w : e, -w * (2.f + w)};
 }
 
 // Two stretches of the recurrence, each (P, H): h -> P h + H, are composed by carry_on for H and
@@ -94,18 +121,79 @@ __device__ __forceinline__ float join(float P, float Q) {
     return v;
 }
 
-// Steps [t0, t0 + kGroup) of a row as fp32; steps outside [0, L) as 0.
+// Steps [t0, t0 + kGroup) of a row as they lie in memory.  `vec`: the group starts on a 16-byte
+// boundary.  Whole groups inside the row [0, L) are read as vectors, the row's ends and rows that lie
+// otherwise element by element; steps outside [0, len) are 0 or anything, and never used.
 template <typename IO>
-__device__ __forceinline__ void load_group(const IO* row, int t0, int L, float (&v)[kGroup]) {
-#pragma unroll
-    for (int e = 0; e < kGroup; ++e) v[e] = (t0 + e >= 0 && t0 + e < L) ? IoTraits<IO>::to_f32(row[t0 + e]) : 0.f;
+struct RawGroup {
+    uint4 v[sizeof(IO) / 2];
+};
+
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
 }
 
 template <typename IO>
-__device__ __forceinline__ void store_group(IO* row, int t0, int L, const float (&v)[kGroup]) {
+__device__ __forceinline__ RawGroup<IO> load_group(const IO* row, int t0, int len, int L, bool vec) {
+    RawGroup<IO> g{};
+    if (t0 >= len) return g;
+    if (vec && t0 >= 0 && t0 + kGroup <= L) {
 #pragma unroll
-    for (int e = 0; e < kGroup; ++e)
-        if (t0 + e >= 0 && t0 + e < L) row[t0 + e] = IoTraits<IO>::from_f32(v[e]);
+        for (int k = 0; k < static_cast<int>(sizeof(IO) / 2); ++k) g.v[k] = ld_stream(reinterpret_cast<const uint4*>(row + t0) + k);
+    } else {
+        uint32_t w[sizeof(IO) * 2] = {};
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e) {
+            if (t0 + e < 0 || t0 + e >= len) continue;
+            if constexpr (sizeof(IO) == 2)
+                w[e / 2] |= static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(row)[t0 + e]) << (e % 2 * 16);
+            else
+                w[e] = reinterpret_cast<const uint32_t*>(row)[t0 + e];
+        }
+#pragma unroll
+        for (int k = 0; k < static_cast<int>(sizeof(IO) / 2); ++k) g.v[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
+    return g;
+}
+
+template <typename IO>
+__device__ __forceinline__ void unpack(const RawGroup<IO>& g, float (&v)[kGroup]) {
+    constexpr int n = Group16<IO>::kN;
+#pragma unroll
+    for (int k = 0; k < kGroup / n; ++k) {
+        float part[n];
+        Group16<IO>::unpack(g.v[k], part);
+#pragma unroll
+        for (int e = 0; e < n; ++e) v[k * n + e] = part[e];
+    }
+}
+
+// The steps of the group that lie in [0, n).
+template <typename IO>
+__device__ __forceinline__ void store_group(IO* row, int t0, int n, bool vec, const float (&v)[kGroup]) {
+    if (vec && t0 >= 0 && t0 + kGroup <= n) {
+        uint4* to = reinterpret_cast<uint4*>(row + t0);
+        if constexpr (sizeof(IO) == 2) {
+            *to = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        } else {
+            reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e)
+            if (t0 + e >= 0 && t0 + e < n) row[t0 + e] = IoTraits<IO>::from_f32(v[e]);
+    }
+}
+
+// A row's groups are laid so that those of x start on 16-byte boundaries: group g holds the steps
+// from g * kGroup - phase.  Operands that lie like x, which dense ones of one shape do, are read and
+// written as vectors at any length of the rows; each operand is looked at by itself.
+template <typename IO>
+__device__ __forceinline__ int phase_of(const IO* row) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(IO));
 }
 
 template <typename IO>
