@@ -76,25 +76,71 @@ __device__ __forceinline__ float softplus_lam(float lam) {
     return fmaf(e, p, fmaxf(lam, 0.f));
 }
 
-// The decay a = e^{-v} and 1 - a^2 = -w (2 + w), w = a - 1, from y = -v log2(e).  Near a = 1 the
-// difference w cancels, so below v = 1/8 the series w = -v (1 - v/2 + v^2/6 - ...) up to v^6 / 720
-// takes its place (the first term left out is 1e-9 of the sum there; above the border the cancellation
-// costs at most 2e-6 of w), and a = 1 + w is then good to half a step.  For both element types: the
-// state and the parameters' gradients are fp32.
-struct Decay {
-    float a, m2;  // m2 = 1 - a^2
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// min that keeps a NaN.
+__device__ __forceinline__ float min_nan(float x, float limit) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(limit));
+    return y;
+}
+
+// Both gates of two steps: rho = sigmoid(r + r_bias), iota = sigmoid(i + i_bias) from kr = -log2(e)
+// r_bias and ki likewise, and Er = e^{-(r + r_bias)}, Ei (1 - rho = Er rho without cancellation).
+// One reciprocal serves a step's two gates, 1 / ((1 + Er)(1 + Ei)), as the special-function unit is
+// the scarcest.  So that the product stays finite a gate below 2^-63 counts as 2^-63.
+struct Gates {
+    float2 rho, iota, Er, Ei;
 };
 
-__device__ __forceinline__ Decay decay_of(float y) {
-    const float e = ex2_mufu(y), x = y * kLn2;
-    float p = fmaf(x, 1.f / 720, 1.f / 120);
-    p = fmaf(x, p, 1.f / 24);
-    p = fmaf(x, p, 1.f / 6);
-    p = fmaf(x, p, 0.5f);
-    p = fmaf(x * x, p, x);
-    const bool near = x > -0.125f;
-    const float w = near ? p : e - 1.f;
-    return {near ? 1.f + w : e, -w * (2.f + w)};
+__device__ __forceinline__ Gates gates_of(float2 r, float2 i, float kr, float ki) {
+    const float2 yr = __ffma2_rn(both(-kLog2e), r, both(kr)), yi = __ffma2_rn(both(-kLog2e), i, both(ki));
+    Gates g;
+    g.Er = make_float2(ex2_mufu(min_nan(yr.x, 63.f)), ex2_mufu(min_nan(yr.y, 63.f)));
+    g.Ei = make_float2(ex2_mufu(min_nan(yi.x, 63.f)), ex2_mufu(min_nan(yi.y, 63.f)));
+    const float2 dr = __fadd2_rn(both(1.f), g.Er), di = __fadd2_rn(both(1.f), g.Ei), d = __fmul2_rn(dr, di);
+    const float2 inv = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+    g.rho = __fmul2_rn(inv, di);
+    g.iota = __fmul2_rn(inv, dr);
+    return g;
+}
+
+// The decay a = e^x and 1 - a^2 = -w (2 + w), w = a - 1, of two steps with x = -v <= 0.  Near a = 1 the
+// difference w cancels, so for v < 1/8 the series w = x (1 + x/2 + x^2/6 + x^3/24 + x^4/120) takes its
+// place (the first term left out is 4e-8 of the sum there; beyond it the cancellation costs at most
+// 2e-6 of w), and a = 1 + w is then good to half a step.  For both element types: the state and the
+// parameters' gradients are fp32.  NEAR: c softplus(lam) < 1/8, so that no step of the channel needs
+// the exponential: channels with a memory of some ten steps or more.
+constexpr float kNear = 0.125f;
+
+struct Decay {
+    float2 a, m2;  // m2 = 1 - a^2
+};
+
+template <bool NEAR>
+__device__ __forceinline__ Decay decay_of(float2 x) {
+    float2 p = __ffma2_rn(x, both(1.f / 120), both(1.f / 24));
+    p = __ffma2_rn(x, p, both(1.f / 6));
+    p = __ffma2_rn(x, p, both(0.5f));
+    float2 w = __ffma2_rn(__fmul2_rn(x, x), p, x);
+    Decay d;
+    if constexpr (NEAR) {
+        d.a = __fadd2_rn(both(1.f), w);
+    } else {
+        const float2 y = __fmul2_rn(x, both(kLog2e));
+        const float2 e = make_float2(ex2_mufu(y.x), ex2_mufu(y.y)), f = __fadd2_rn(e, both(-1.f));
+        w = make_float2(x.x > -kNear ? w.x : f.x, x.y > -kNear ? w.y : f.y);
+        const float2 near = __fadd2_rn(both(1.f), w);
+        d.a = make_float2(x.x > -kNear ? near.x : e.x, x.y > -kNear ? near.y : e.y);
+    }
+    d.m2 = __fmul2_rn(w, __ffma2_rn(both(-1.f), w, both(-2.f)));
+    return d;
+}
+
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+    const float2 y = __fmul2_rn(both(-kLog2e), z);
+    const float2 d = __fadd2_rn(both(1.f), make_float2(ex2_mufu(y.x), ex2_mufu(y.y)));
+    return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
 
 // Two stretches of the recurrence, each (P, H): h -> P h + H, are composed by carry_on for H and
@@ -158,33 +204,38 @@ __device__ __forceinline__ RawGroup<IO> load_group(const IO* row, int t0, int le
     return g;
 }
 
+constexpr int kPairs = kGroup / 2;
+
+// Step e of a group kept as pairs of steps.
+__device__ __forceinline__ float& step_of(float2 (&v)[kPairs], int e) { return e % 2 ? v[e / 2].y : v[e / 2].x; }
+
 template <typename IO>
-__device__ __forceinline__ void unpack(const RawGroup<IO>& g, float (&v)[kGroup]) {
+__device__ __forceinline__ void unpack(const RawGroup<IO>& g, float2 (&v)[kPairs]) {
     constexpr int n = Group16<IO>::kN;
 #pragma unroll
     for (int k = 0; k < kGroup / n; ++k) {
         float part[n];
         Group16<IO>::unpack(g.v[k], part);
 #pragma unroll
-        for (int e = 0; e < n; ++e) v[k * n + e] = part[e];
+        for (int e = 0; e < n; e += 2) v[(k * n + e) / 2] = make_float2(part[e], part[e + 1]);
     }
 }
 
 // The steps of the group that lie in [0, n).
 template <typename IO>
-__device__ __forceinline__ void store_group(IO* row, int t0, int n, bool vec, const float (&v)[kGroup]) {
+__device__ __forceinline__ void store_group(IO* row, int t0, int n, bool vec, float2 (&v)[kPairs]) {
     if (vec && t0 >= 0 && t0 + kGroup <= n) {
         uint4* to = reinterpret_cast<uint4*>(row + t0);
         if constexpr (sizeof(IO) == 2) {
-            *to = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+            *to = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
         } else {
-            reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            reinterpret_cast<float4*>(to)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+            reinterpret_cast<float4*>(to)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
         }
     } else {
 #pragma unroll
         for (int e = 0; e < kGroup; ++e)
-            if (t0 + e >= 0 && t0 + e < n) row[t0 + e] = IoTraits<IO>::from_f32(v[e]);
+            if (t0 + e >= 0 && t0 + e < n) row[t0 + e] = IoTraits<IO>::from_f32(step_of(v, e));
     }
 }
 

@@ -11,6 +11,8 @@
 // joins their pairs.  That is for few long rows, which could not fill the GPU's warps otherwise.
 #pragma once
 
+#include <type_traits>
+
 #include "gated_math.cuh"
 
 namespace ssm {
@@ -72,7 +74,8 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     const int phase = phase_of(x);
     const bool vr = phase_of(r) == phase, vi = phase_of(i) == phase, vz = GATE && phase_of(z) == phase, vy = phase_of(y) == phase;
     const unsigned char* reset = RESET ? p.reset + static_cast<long long>(b) * p.L : nullptr;
-    const float rate = -p.c * softplus_lam(p.lam[d]) * kLog2e;
+    const float rate = -p.c * softplus_lam(p.lam[d]);
+    const bool near = rate > -kNear;
     const float rb = -kLog2e * (p.r_bias ? p.r_bias[d] : 0.f), ib = -kLog2e * (p.i_bias ? p.i_bias[d] : 0.f);
     float carry = p.h0 && valid ? p.h0[row] : 0.f;
     float* ckpt = p.ckpt ? p.ckpt + sizeof(CkptHeader) / 4 + row * p.ckpt_row : nullptr;
@@ -89,7 +92,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     int round = 0;
 #pragma unroll 1
     for (int t = -phase; SEG == 32 ? t < len : __any_sync(kAll, t < len); t += stride, t0 += stride, ++round) {
-        float a[kGroup], u[kGroup], v[kGroup], w[kGroup];
+        float2 a[kPairs], u[kPairs], v[kPairs], w[kPairs];
         unpack<IO>(nx, u);
         unpack<IO>(nr, v);
         unpack<IO>(ni, w);
@@ -99,25 +102,37 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         nr = load_group(r, t0 + stride, len, p.L, vr);
         ni = load_group(i, t0 + stride, len, p.L, vi);
         if (GATE) nz = load_group(z, t0 + stride, len, p.L, vz);
-        const bool whole = t0 >= 0 && t0 + kGroup <= len;
+        const auto coefficients = [&](auto near_tag) {
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e) {
-            const Decay dec = decay_of(rate * rcp_approx(1.f + ex2_mufu(fmaf(-kLog2e, v[e], rb))));
-            a[e] = dec.a;
-            float m = sqrt_approx(dec.m2);
-            if (RESET && t0 + e >= 0 && t0 + e < len && reset[t0 + e]) a[e] = kCut, m = 1.f;
-            u[e] *= m * rcp_approx(1.f + ex2_mufu(fmaf(-kLog2e, w[e], ib)));
-        }
-        if (!whole) {
+            for (int k = 0; k < kPairs; ++k) {
+                const Gates gt = gates_of(v[k], w[k], rb, ib);
+                const Decay dec = decay_of<decltype(near_tag)::value>(__fmul2_rn(both(rate), gt.rho));
+                a[k] = dec.a;
+                v[k] = make_float2(sqrt_approx(dec.m2.x), sqrt_approx(dec.m2.y));
+                u[k] = __fmul2_rn(u[k], gt.iota);
+            }
+        };
+        if (near)
+            coefficients(std::true_type{});
+        else
+            coefficients(std::false_type{});
+        if (RESET && t0 < len) {
 #pragma unroll
             for (int e = 0; e < kGroup; ++e)
-                if (t0 + e < 0 || t0 + e >= len) a[e] = 1.f, u[e] = 0.f;
+                if (t0 + e >= 0 && t0 + e < len && reset[t0 + e]) step_of(a, e) = kCut, step_of(v, e) = 1.f;
         }
-        float P = a[0], H = u[0];
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) u[k] = __fmul2_rn(u[k], v[k]);
+        if (t0 < 0 || t0 + kGroup > len) {
+#pragma unroll
+            for (int e = 0; e < kGroup; ++e)
+                if (t0 + e < 0 || t0 + e >= len) step_of(a, e) = 1.f, step_of(u, e) = 0.f;
+        }
+        float P = a[0].x, H = u[0].x;
 #pragma unroll
         for (int e = 1; e < kGroup; ++e) {
-            H = carry_on<RESET>(a[e], H, u[e]);
-            P = join<RESET>(P, a[e]);
+            H = carry_on<RESET>(step_of(a, e), H, step_of(u, e));
+            P = join<RESET>(P, step_of(a, e));
         }
 #pragma unroll
         for (int s = 1; s < SEG; s *= 2) {
@@ -138,11 +153,11 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         }
         if (ckpt && t0 < len) ckpt[(t0 + phase) / kGroup] = h;
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e) u[e] = h = carry_on<RESET>(a[e], h, u[e]);
+        for (int e = 0; e < kGroup; ++e) step_of(u, e) = h = carry_on<RESET>(step_of(a, e), h, step_of(u, e));
         if (GATE) {
             unpack<IO>(zc, w);
 #pragma unroll
-            for (int e = 0; e < kGroup; ++e) u[e] *= silu_f32(w[e]);
+            for (int k = 0; k < kPairs; ++k) u[k] = __fmul2_rn(u[k], __fmul2_rn(w[k], sigmoid2(w[k])));
         }
         if (y) store_group(y, t0, len, vy, u);
     }
@@ -172,15 +187,16 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
                vdz = GATE && phase_of(dz) == phase;
     const unsigned char* reset = RESET ? p.reset + static_cast<long long>(b) * p.L : nullptr;
     const float* ckpt = p.ckpt + sizeof(CkptHeader) / 4 + row * p.ckpt_row;
-    const float rate = -p.c * softplus_lam(p.lam[d]) * kLog2e;
+    const float rate = -p.c * softplus_lam(p.lam[d]);
+    const bool near = rate > -kNear;
     const float rb = -kLog2e * (p.r_bias ? p.r_bias[d] : 0.f), ib = -kLog2e * (p.i_bias ? p.i_bias[d] : 0.f);
     float carry = p.dlast && valid ? p.dlast[row] : 0.f;  // a_{t+1} g_{t+1}: what the steps after the tile send back
-    float sumT = 0.f, sumr = 0.f, sumi = 0.f;
+    float2 sumT = both(0.f), sumr = both(0.f), sumi = both(0.f);
 
     const int stride = at.parts * kStep;
     int t = (len + phase + stride - 1) / stride * stride - phase;  // where the rounds with steps end
     for (int t0 = t + (at.part * SEG + at.lane) * kGroup; t0 < L; t0 += stride) {  // padding: zeros
-        const float zero[kGroup] = {};
+        float2 zero[kPairs] = {};
         store_group(dx, t0, L, vdx, zero);
         store_group(dr, t0, L, vdr, zero);
         store_group(di, t0, L, vdi, zero);
@@ -192,7 +208,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         const int t0 = t + (at.part * SEG + at.lane) * kGroup;
         // (a short row that is done while others of its warp go on: t0 below its first step, no steps inside)
         const int end = t >= -phase ? len : -phase;
-        float a[kGroup], g[kGroup], kx[kGroup], ki[kGroup], kT[kGroup], kr[kGroup];
+        float2 a[kPairs], g[kPairs], kx[kPairs], ki[kPairs], kT[kPairs], kr[kPairs], b[kPairs], ax[kPairs];
         const RawGroup<IO> rz = GATE ? load_group(z, t0, end, p.L, vz) : RawGroup<IO>{};
         {
             const RawGroup<IO> rx = load_group(x, t0, end, p.L, vx), rr = load_group(r, t0, end, p.L, vr),
@@ -203,52 +219,77 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
             unpack<IO>(rg, g);
         }
         float h = t0 >= -phase && t0 < end ? ckpt[(t0 + phase) / kGroup] : 0.f;
-        float zv[kGroup], gz[kGroup];
-        if (GATE) unpack<IO>(rz, zv);
+        // what g_t is to be multiplied by, for each gradient:
+        //   dx  kx = m iota         di  ki = b (1 - iota), b = m iota x
+        //   T   kT = a (iota x a v / m - h_{t-1} v), its first part here      dr  T kr, kr = 1 - rho
+        const auto coefficients = [&](auto near_tag) {
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e) {
-            const bool cut = RESET && t0 + e >= 0 && t0 + e < end && reset[t0 + e];
-            const float Er = ex2_mufu(fmaf(-kLog2e, kr[e], rb)), Ei = ex2_mufu(fmaf(-kLog2e, ki[e], ib));
-            const float rho = rcp_approx(1.f + Er), iota = rcp_approx(1.f + Ei);
-            const float yv = rate * rho;
-            const Decay dec = decay_of(yv);
-            a[e] = dec.a;
-            const float rs = rsqrt_approx(fmaxf(dec.m2, 1e-30f));  // v -> 0: m and v / m go to 0
-            float m = dec.m2 * rs;
-            const float v = -kLn2 * yv, q = v * rs;
-            if (cut) a[e] = kCut, m = 1.f;
-            const float ux = iota * kx[e];
-            // what g_t is to be multiplied by, for each gradient
-            const float T = cut ? 0.f : a[e] * (ux * a[e] * q - h * v);
-            const float before = h;
-            h = carry_on<RESET>(a[e], h, m * ux);
-            kT[e] = T;
-            kr[e] = T * (fminf(Er, 1e38f) * rho);  // 1 - rho = Er rho, without cancellation
-            ki[e] = m * ux * (fminf(Ei, 1e38f) * iota);
-            kx[e] = m * iota;
-            if (GATE) {
-                const float sig = rcp_approx(1.f + ex2_mufu(-kLog2e * zv[e]));
-                gz[e] = g[e] * h * sig * fmaf(zv[e], 1.f - sig, 1.f);
-                g[e] *= zv[e] * sig;
+            for (int k = 0; k < kPairs; ++k) {
+                const Gates gt = gates_of(kr[k], ki[k], rb, ib);
+                const float2 xv = __fmul2_rn(both(rate), gt.rho);  // -v
+                const Decay dec = decay_of<decltype(near_tag)::value>(xv);
+                // v -> 0: m and v / m go to 0
+                const float2 rs = make_float2(rsqrt_approx(fmaxf(dec.m2.x, 1e-30f)), rsqrt_approx(fmaxf(dec.m2.y, 1e-30f)));
+                const float2 ux = __fmul2_rn(gt.iota, kx[k]), m = __fmul2_rn(dec.m2, rs);
+                a[k] = dec.a;
+                ax[k] = __fmul2_rn(dec.a, xv);
+                kT[k] = __fmul2_rn(__fmul2_rn(make_float2(-dec.a.x, -dec.a.y), __fmul2_rn(ax[k], rs)), ux);
+                kr[k] = __fmul2_rn(gt.Er, gt.rho);
+                kx[k] = __fmul2_rn(m, gt.iota);
+                b[k] = __fmul2_rn(m, ux);
+                ki[k] = __fmul2_rn(b[k], __fmul2_rn(gt.Ei, gt.iota));
+                if constexpr (RESET) {
+                    const int t = t0 + 2 * k;
+                    const bool c0 = t >= 0 && t < end && reset[t], c1 = t + 1 >= 0 && t + 1 < end && reset[t + 1];
+                    if (c0) a[k].x = kCut, ax[k].x = kT[k].x = 0.f, kx[k].x = gt.iota.x, b[k].x = ux.x, ki[k].x = ux.x * (gt.Ei.x * gt.iota.x);
+                    if (c1) a[k].y = kCut, ax[k].y = kT[k].y = 0.f, kx[k].y = gt.iota.y, b[k].y = ux.y, ki[k].y = ux.y * (gt.Ei.y * gt.iota.y);
+                }
             }
-            if (t0 + e < 0) h = before;
-        }
+        };
+        if (near)
+            coefficients(std::true_type{});
+        else
+            coefficients(std::false_type{});
         const bool whole = t0 >= 0 && t0 + kGroup <= end;
         if (!whole) {
 #pragma unroll
             for (int e = 0; e < kGroup; ++e)
                 if (t0 + e < 0 || t0 + e >= end) {
-                    a[e] = 1.f;
-                    g[e] = kT[e] = kr[e] = ki[e] = kx[e] = 0.f;
-                    if (GATE) gz[e] = 0.f;
+                    step_of(a, e) = 1.f;
+                    step_of(g, e) = step_of(kT, e) = step_of(ax, e) = step_of(kr, e) = step_of(ki, e) = step_of(kx, e) = step_of(b, e) = 0.f;
                 }
         }
-        if (GATE && t >= -phase) store_group(dz, t0, L, vdz, gz);
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e) {  // b becomes the states
+            const float term = fmaf(h, step_of(ax, e), step_of(kT, e));
+            step_of(kT, e) = RESET && is_cut(step_of(a, e)) ? 0.f : term;
+            step_of(b, e) = h = carry_on<RESET>(step_of(a, e), h, step_of(b, e));
+        }
+        if (GATE) {
+            float2 zv[kPairs];
+            unpack<IO>(rz, zv);
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) {
+                const float2 sig = sigmoid2(zv[k]), zs = __fmul2_rn(zv[k], sig);
+                // silu' = sig (1 + z (1 - sig)) = sig + z sig - z sig sig
+                const float2 slope = __ffma2_rn(make_float2(-zs.x, -zs.y), sig, __fadd2_rn(sig, zs));
+                b[k] = __fmul2_rn(__fmul2_rn(g[k], b[k]), slope);
+                g[k] = __fmul2_rn(g[k], zs);
+            }
+            if (!whole) {
+#pragma unroll
+                for (int e = 0; e < kGroup; ++e)
+                    if (t0 + e < 0 || t0 + e >= end) step_of(g, e) = step_of(b, e) = 0.f;
+            }
+            if (t >= -phase) store_group(dz, t0, L, vdz, b);
+        }
         float P = 1.f, S = 0.f;
 #pragma unroll
+        for (int k = 0; k < kPairs; ++k) ax[k] = __fmul2_rn(a[k], g[k]);
+#pragma unroll
         for (int e = kGroup - 1; e >= 0; --e) {
-            S = carry_on<RESET>(a[e], g[e] + S, 0.f);
-            P = join<RESET>(P, a[e]);
+            S = carry_on<RESET>(step_of(a, e), S, step_of(ax, e));
+            P = join<RESET>(P, step_of(a, e));
         }
 #pragma unroll
         for (int s = 1; s < SEG; s *= 2) {
@@ -269,19 +310,23 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         }
 #pragma unroll
         for (int e = kGroup - 1; e >= 0; --e) {
-            const float ge = g[e] + s;
-            s = carry_on<RESET>(a[e], ge, 0.f);
-            sumT = fmaf(ge, kT[e], sumT);
-            kx[e] *= ge;
-            kr[e] *= ge;
-            ki[e] *= ge;
-            sumr += kr[e];
-            sumi += ki[e];
+            step_of(g, e) += s;
+            s = carry_on<RESET>(step_of(a, e), s, step_of(ax, e));
+        }
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+            const float2 T = __fmul2_rn(g[k], kT[k]);
+            kx[k] = __fmul2_rn(g[k], kx[k]);
+            kr[k] = __fmul2_rn(T, kr[k]);
+            ki[k] = __fmul2_rn(g[k], ki[k]);
+            sumT = __fadd2_rn(sumT, T);
+            sumr = __fadd2_rn(sumr, kr[k]);
+            sumi = __fadd2_rn(sumi, ki[k]);
         }
         if (!whole) {  // (0 times an infinite gradient of the last state)
 #pragma unroll
             for (int e = 0; e < kGroup; ++e)
-                if (t0 + e >= end) kx[e] = kr[e] = ki[e] = 0.f;
+                if (t0 + e >= end) step_of(kx, e) = step_of(kr, e) = step_of(ki, e) = 0.f;
         }
         if (t >= -phase) {
             store_group(dx, t0, L, vdx, kx);
@@ -291,14 +336,15 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     }
     if (p.dh0 && valid && at.part == 0 && at.lane == 0) p.dh0[row] = carry;
     if (p.part) {
+        float sT = sumT.x + sumT.y, sr = sumr.x + sumr.y, si = sumi.x + sumi.y;
 #pragma unroll
         for (int s = SEG / 2; s; s /= 2) {
-            sumT += __shfl_xor_sync(kAll, sumT, s, SEG);
-            sumr += __shfl_xor_sync(kAll, sumr, s, SEG);
-            sumi += __shfl_xor_sync(kAll, sumi, s, SEG);
+            sT += __shfl_xor_sync(kAll, sT, s, SEG);
+            sr += __shfl_xor_sync(kAll, sr, s, SEG);
+            si += __shfl_xor_sync(kAll, si, s, SEG);
         }
         if constexpr (SPLIT) {
-            if (at.lane == 0) part_sums[0][at.part] = sumT, part_sums[1][at.part] = sumr, part_sums[2][at.part] = sumi;
+            if (at.lane == 0) part_sums[0][at.part] = sT, part_sums[1][at.part] = sr, part_sums[2][at.part] = si;
             __syncthreads();
             if (threadIdx.x < 3) {
                 float s = 0.f;
@@ -306,7 +352,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
                 p.part[threadIdx.x * rows + row] = s;
             }
         } else if (valid && at.lane == 0) {
-            p.part[row] = sumT, p.part[rows + row] = sumr, p.part[2 * rows + row] = sumi;
+            p.part[row] = sT, p.part[rows + row] = sr, p.part[2 * rows + row] = si;
         }
     }
 }

@@ -83,13 +83,22 @@ __global__ void __launch_bounds__(kStepThreads) gated_step_kernel(const GatedSte
     }
     if (d >= p.dim) return;
 #pragma unroll
-    for (int k = 0; k < kStepChannels; ++k) rate[k] = -p.c * softplus_lam(rate[k]) * kLog2e;
+    for (int k = 0; k < kStepChannels; ++k) rate[k] = -p.c * softplus_lam(rate[k]);
     for (int row = b;;) {
 #pragma unroll
-        for (int k = 0; k < kStepChannels; ++k) {
-            const Decay dec = decay_of(rate[k] * rcp_approx(1.f + ex2_mufu(-kLog2e * (r[k] + rb[k]))));
-            h[k] = fmaf(dec.a, h[k], sqrt_approx(dec.m2) * rcp_approx(1.f + ex2_mufu(-kLog2e * (i[k] + ib[k]))) * x[k]);
-            x[k] = GATE ? h[k] * silu_f32(z[k]) : h[k];
+        for (int k = 0; k < kStepChannels; k += 2) {
+            const float2 hv = make_float2(h[k], h[k + 1]), xv = make_float2(x[k], x[k + 1]);
+            const Gates gt = gates_of(make_float2(r[k] + rb[k], r[k + 1] + rb[k + 1]), make_float2(i[k] + ib[k], i[k + 1] + ib[k + 1]), 0.f, 0.f);
+            const Decay dec = decay_of<false>(__fmul2_rn(make_float2(rate[k], rate[k + 1]), gt.rho));
+            const float2 m = make_float2(sqrt_approx(dec.m2.x), sqrt_approx(dec.m2.y));
+            const float2 now = __ffma2_rn(dec.a, hv, __fmul2_rn(__fmul2_rn(m, gt.iota), xv));
+            h[k] = now.x, h[k + 1] = now.y;
+            float2 out = now;
+            if (GATE) {
+                const float2 zv = make_float2(z[k], z[k + 1]);
+                out = __fmul2_rn(now, __fmul2_rn(zv, sigmoid2(zv)));
+            }
+            x[k] = out.x, x[k + 1] = out.y;
         }
         store4(static_cast<IO*>(p.y) + row * p.y_stride, d, p.dim, vec, x);
         if (!again) break;
