@@ -18,7 +18,7 @@ inline GatedShape gated_shape(long long rows, int L) {
     if (L <= 2 * ssm::kGroup) return {2, 1};
     if (L <= 8 * ssm::kGroup) return {8, 1};
     int split = 1;
-    while (split < ssm::kMaxSplit && rows * split < 148 * 16 && split * ssm::kTile < L) split *= 2;
+    while (split < ssm::kMaxSplit && rows * split < 148 * 16 && split * 32 * ssm::kGroup < L) split *= 2;
     return {32, split};
 }
 
@@ -42,7 +42,10 @@ ssm_status_t launch_gated(ssm::GatedParams p, bool backward, cudaStream_t stream
                                   : (reset ? gated_kernel<IO, false, true>(shape, backward) : gated_kernel<IO, false, false>(shape, backward));
     const int block = shape.split > 1 ? shape.split * 32 : ssm::kGatedWarps * 32;
     const long long per_block = shape.split > 1 ? 1 : block / shape.seg;
-    kern<<<static_cast<unsigned>((rows + per_block - 1) / per_block), block, 0, stream>>>(p);
+    const int smem = backward ? ssm::bwd_smem<IO>(gate, block) : 0;
+    if (smem > 46 * 1024 &&  // (with the static part of it, past the 48 KB that need no asking)
+        !ensure_smem_attr(reinterpret_cast<const void*>(kern), smem)) return SSM_ERR_LAUNCH;
+    kern<<<static_cast<unsigned>((rows + per_block - 1) / per_block), block, smem, stream>>>(p);
     return launch_status();
 }
 

@@ -41,8 +41,25 @@ struct CkptHeader {
     unsigned base, bs, ds, pad;
 };
 
-constexpr int kGroup = 8;           // steps that a lane holds at once, and between two checkpoints
-constexpr int kTile = 32 * kGroup;  // steps of a warp's tile
+constexpr int kGroup = 8;  // steps between two checkpoints
+
+#ifndef FWD_STEPS
+#define FWD_STEPS 16
+#endif
+#ifndef BWD_STAGES
+#define BWD_STAGES 3
+#endif
+#ifndef BWD_STAGES32
+#define BWD_STAGES32 0
+#endif
+#ifndef F32_AHEAD
+#define F32_AHEAD 1
+#endif
+// Steps that a lane holds at once.
+template <typename IO> constexpr int kFwdSteps = sizeof(IO) == 2 ? FWD_STEPS : 8;
+constexpr int kBwdSteps = 8;
+// Stages of the backward's ring; 0: none.
+template <typename IO> constexpr int kBwdStages = sizeof(IO) == 2 ? BWD_STAGES : BWD_STAGES32;
 
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
@@ -143,36 +160,53 @@ __device__ __forceinline__ float2 sigmoid2(float2 z) {
     return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
 
+// silu(z) of two steps for an output of type IO, as gate_silu: for bf16 by the tanh form, one
+// special-function operation instead of two, whose 2^-12 |z| stays below the output's half step of
+// 2^-9 where z > -1 and below 2^-9 max |silu| behind.
+template <typename IO>
+__device__ __forceinline__ float2 gate_silu2(float2 z) {
+    if constexpr (sizeof(IO) == 2) {
+        const float2 half = __fmul2_rn(both(0.5f), z);
+        float2 t;
+        asm("tanh.approx.f32 %0, %1;" : "=f"(t.x) : "f"(half.x));
+        asm("tanh.approx.f32 %0, %1;" : "=f"(t.y) : "f"(half.y));
+        return __ffma2_rn(half, t, half);
+    } else {
+        return __fmul2_rn(z, sigmoid2(z));
+    }
+}
+
 // Two stretches of the recurrence, each (P, H): h -> P h + H, are composed by carry_on for H and
-// join for P.  A reset has the coefficient kCut, whose sign marks it (decays are never negative):
-// the mark stays with every product that spans it, and what lies before a marked stretch is
-// dropped rather than multiplied by 0, so that an infinity or NaN cannot pass.  A product that
-// merely underflows has no mark, and lets them pass as the steps one by one would.
+// join for P.  A reset has the coefficient kCut = -0, and CUT = false multiplies by it: enough as
+// long as all states are finite.  Infinities and NaNs stay with every state that follows, so a look at
+// the last one tells.  Then CUT = true: the sign marks the reset (decays are never negative), the mark
+// stays with every product that spans it, and what lies before a marked stretch is dropped, so
+// that an infinity or NaN cannot pass.  A product that merely underflows has no mark, and lets them
+// pass as the steps one by one would.
 constexpr float kCut = -0.f;
 
 __device__ __forceinline__ bool is_cut(float P) { return __float_as_int(P) < 0; }
 
-template <bool RESET>
+template <bool CUT>
 __device__ __forceinline__ float carry_on(float P, float earlier, float H) {
     const float v = fmaf(P, earlier, H);
-    if constexpr (RESET) return is_cut(P) ? H : v;
+    if constexpr (CUT) return is_cut(P) ? H : v;
     return v;
 }
 
-template <bool RESET>
+template <bool CUT>
 __device__ __forceinline__ float join(float P, float Q) {
     const float v = P * Q;
-    if constexpr (RESET)
+    if constexpr (CUT)
         return __int_as_float(__float_as_int(v) | ((__float_as_int(P) | __float_as_int(Q)) & 0x80000000));
     return v;
 }
 
-// Steps [t0, t0 + kGroup) of a row as they lie in memory.  `vec`: the group starts on a 16-byte
-// boundary.  Whole groups inside the row [0, L) are read as vectors, the row's ends and rows that lie
-// otherwise element by element; steps outside [0, len) are 0 or anything, and never used.
-template <typename IO>
-struct RawGroup {
-    uint4 v[sizeof(IO) / 2];
+// N consecutive steps of a row as they lie in memory.
+template <typename IO, int N>
+struct Raw {
+    static constexpr int kVecs = N * sizeof(IO) / 16;
+    uint4 v[kVecs];
 };
 
 __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
@@ -181,39 +215,105 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
     return v;
 }
 
-template <typename IO>
-__device__ __forceinline__ RawGroup<IO> load_group(const IO* row, int t0, int len, int L, bool vec) {
-    RawGroup<IO> g{};
-    if (t0 >= len) return g;
-    if (vec && t0 >= 0 && t0 + kGroup <= L) {
+template <typename IO, int N>
+__device__ __forceinline__ void load_vectors(const IO* row, int t0, Raw<IO, N>& g) {
+    const uint4* q = reinterpret_cast<const uint4*>(row + t0);
 #pragma unroll
-        for (int k = 0; k < static_cast<int>(sizeof(IO) / 2); ++k) g.v[k] = ld_stream(reinterpret_cast<const uint4*>(row + t0) + k);
-    } else {
-        uint32_t w[sizeof(IO) * 2] = {};
-#pragma unroll
-        for (int e = 0; e < kGroup; ++e) {
-            if (t0 + e < 0 || t0 + e >= len) continue;
-            if constexpr (sizeof(IO) == 2)
-                w[e / 2] |= static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(row)[t0 + e]) << (e % 2 * 16);
-            else
-                w[e] = reinterpret_cast<const uint32_t*>(row)[t0 + e];
-        }
-#pragma unroll
-        for (int k = 0; k < static_cast<int>(sizeof(IO) / 2); ++k) g.v[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-    }
-    return g;
+    for (int k = 0; k < Raw<IO, N>::kVecs; ++k) g.v[k] = ld_stream(q + k);
 }
 
-constexpr int kPairs = kGroup / 2;
+// The row's ends, and rows that lie otherwise than the groups do: element by element, 0 outside [0, len).
+template <typename IO, int N>
+__device__ __forceinline__ void load_elements(const IO* row, int t0, int len, Raw<IO, N>& g) {
+    constexpr int kWords = N * sizeof(IO) / 4;
+    uint32_t w[kWords] = {};
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        if (t0 + e < 0 || t0 + e >= len) continue;
+        if constexpr (sizeof(IO) == 2)
+            w[e / 2] |= static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(row)[t0 + e]) << (e % 2 * 16);
+        else
+            w[e] = reinterpret_cast<const uint32_t*>(row)[t0 + e];
+    }
+#pragma unroll
+    for (int k = 0; k < kWords / 4; ++k) g.v[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+}
 
-// Step e of a group kept as pairs of steps.
-__device__ __forceinline__ float& step_of(float2 (&v)[kPairs], int e) { return e % 2 ? v[e / 2].y : v[e / 2].x; }
+// Steps [t0, t0 + N) of the operands, those of them inside [0, len); the others are anything.
+template <typename IO, int N, int IN>
+__device__ __forceinline__ void load_steps(const IO* const (&in)[IN], const bool (&vec)[IN], bool all_vec, int t0, int len, int L,
+                                           Raw<IO, N> (&g)[IN]) {
+    const bool whole = t0 >= 0 && t0 + N <= L;
+    if (all_vec && whole && t0 < len) {
+#pragma unroll
+        for (int k = 0; k < IN; ++k) load_vectors(in[k], t0, g[k]);
+    } else if (t0 < len && t0 + N > 0) {
+#pragma unroll
+        for (int k = 0; k < IN; ++k) {
+            if (vec[k] && whole)
+                load_vectors(in[k], t0, g[k]);
+            else
+                load_elements(in[k], t0, len, g[k]);
+        }
+    }
+}
 
-template <typename IO>
-__device__ __forceinline__ void unpack(const RawGroup<IO>& g, float2 (&v)[kPairs]) {
+// The same a few tiles ahead: every thread copies its own steps of the tiles to come into its own slots
+// of shared memory and reads them from there when their turn comes.  No other thread touches them,
+// so there is nothing to wait for but the thread's own copies; and the tiles under way take no
+// registers.
+template <typename IO, int N, int IN>
+struct Ring {
+    static constexpr int kV = Raw<IO, N>::kVecs, kVecs = IN * kV;  // 16-byte slots of an operand, of a stage
+    __device__ static uint4* slot(uint4* ring, int stage, int k) { return ring + (stage * kVecs + k) * blockDim.x + threadIdx.x; }
+
+    __device__ static void copy(uint4* ring, int stage, int k, const IO* row, int t0) {
+        const uint4* q = reinterpret_cast<const uint4*>(row + t0);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) cp_async_16(slot(ring, stage, k * kV + j), q + j, 16);
+    }
+    // One group of copies.
+    __device__ static void load(uint4* ring, int stage, const IO* const (&in)[IN], const bool (&vec)[IN], bool all_vec, int t0, int len, int L) {
+        const bool whole = t0 >= 0 && t0 + N <= L;
+        if (all_vec && whole && t0 < len) {
+#pragma unroll
+            for (int k = 0; k < IN; ++k) copy(ring, stage, k, in[k], t0);
+        } else if (t0 < len && t0 + N > 0) {
+#pragma unroll
+            for (int k = 0; k < IN; ++k) {
+                if (vec[k] && whole) {
+                    copy(ring, stage, k, in[k], t0);
+                } else {
+                    Raw<IO, N> g;
+                    load_elements(in[k], t0, len, g);
+#pragma unroll
+                    for (int j = 0; j < kV; ++j) *slot(ring, stage, k * kV + j) = g.v[j];
+                }
+            }
+        }
+        cp_async_commit();
+    }
+    __device__ static Raw<IO, N> read(uint4* ring, int stage, int k) {
+        Raw<IO, N> s;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) s.v[j] = *slot(ring, stage, k * kV + j);
+        return s;
+    }
+};
+
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < __int_as_float(0x7f800000); }
+
+// Step e of steps kept as pairs.
+template <int PAIRS>
+__device__ __forceinline__ float& step_of(float2 (&v)[PAIRS], int e) {
+    return e % 2 ? v[e / 2].y : v[e / 2].x;
+}
+
+template <typename IO, int N>
+__device__ __forceinline__ void unpack(const Raw<IO, N>& g, float2 (&v)[N / 2]) {
     constexpr int n = Group16<IO>::kN;
 #pragma unroll
-    for (int k = 0; k < kGroup / n; ++k) {
+    for (int k = 0; k < N / n; ++k) {
         float part[n];
         Group16<IO>::unpack(g.v[k], part);
 #pragma unroll
@@ -221,22 +321,53 @@ __device__ __forceinline__ void unpack(const RawGroup<IO>& g, float2 (&v)[kPairs
     }
 }
 
-// The steps of the group that lie in [0, n).
-template <typename IO>
-__device__ __forceinline__ void store_group(IO* row, int t0, int n, bool vec, float2 (&v)[kPairs]) {
-    if (vec && t0 >= 0 && t0 + kGroup <= n) {
-        uint4* to = reinterpret_cast<uint4*>(row + t0);
-        if constexpr (sizeof(IO) == 2) {
-            *to = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
-        } else {
-            reinterpret_cast<float4*>(to)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-            reinterpret_cast<float4*>(to)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
-        }
+template <typename IO, int PAIRS>
+__device__ __forceinline__ void store_vectors(IO* row, int t0, float2 (&v)[PAIRS]) {
+    uint4* to = reinterpret_cast<uint4*>(row + t0);
+    if constexpr (sizeof(IO) == 2) {
+#pragma unroll
+        for (int k = 0; k < PAIRS; k += 4)
+            to[k / 4] = make_uint4(pack_bf16x2(v[k].x, v[k].y), pack_bf16x2(v[k + 1].x, v[k + 1].y), pack_bf16x2(v[k + 2].x, v[k + 2].y),
+                                   pack_bf16x2(v[k + 3].x, v[k + 3].y));
     } else {
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e)
+        for (int k = 0; k < PAIRS; k += 2) reinterpret_cast<float4*>(to)[k / 2] = make_float4(v[k].x, v[k].y, v[k + 1].x, v[k + 1].y);
+    }
+}
+
+// The steps that lie in [0, n); `vec`: as vectors where all of them do.
+template <typename IO, int PAIRS>
+__device__ __forceinline__ void store_steps(IO* row, int t0, int n, bool vec, float2 (&v)[PAIRS]) {
+    if (vec && t0 >= 0 && t0 + 2 * PAIRS <= n) {
+        store_vectors(row, t0, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 2 * PAIRS; ++e)
             if (t0 + e >= 0 && t0 + e < n) row[t0 + e] = IoTraits<IO>::from_f32(step_of(v, e));
     }
+}
+
+// The reset flags of 8 steps, a byte each, 0 outside [0, len).  A row's flags lie at any alignment: two
+// aligned words and a shift, or bytes where those words would reach out of the array [begin, end).
+__device__ __forceinline__ unsigned long long reset_flags(const unsigned char* row, int t0, int len, const unsigned char* begin,
+                                                          const unsigned char* end) {
+    const unsigned char* q = row + t0;
+    const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(q) & 7u);
+    unsigned long long flags = 0;
+    if (t0 >= 0 && t0 + 8 <= len && q - off >= begin && q - off + 16 <= end) {
+        const auto* w = reinterpret_cast<const unsigned long long*>(q - off);
+        flags = w[0] >> (8 * off);
+        if (off) flags |= w[1] << (64 - 8 * off);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (t0 + e >= 0 && t0 + e < len) flags |= static_cast<unsigned long long>(q[e]) << (8 * e);
+    }
+    return flags;
+}
+
+__device__ __forceinline__ bool flag_of(unsigned long long flags, int e) {
+    return (static_cast<unsigned>(flags >> (e / 4 * 32)) & (0xffu << (e % 4 * 8))) != 0;
 }
 
 // A row's groups are laid so that those of x start on 16-byte boundaries: group g holds the steps

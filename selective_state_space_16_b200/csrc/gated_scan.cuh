@@ -1,8 +1,7 @@
 // gated_scan.cuh -- forward and backward of the gated linear recurrence over whole sequences.
 //
-// A row (b, d) is walked in tiles: lane k of SEG lanes holds 8 consecutive steps (a group).  The
-// recurrence is composed of pairs (P, H), h -> P h + H: each lane forms its group's pair, rounds of
-// shuffles give every lane the state before its first step, and the lane runs its steps again from
+// A row (b, d) is walked in tiles: lane k of SEG lanes holds 8 or 16 consecutive steps.  The recurrence
+// is composed of pairs (P, H), h -> P h + H: each lane forms its steps' pair, rounds of shuffles give every lane the state before its first step, and the lane runs its steps again from
 // there.  The backward does the same from the last tile to the first; the states come from the
 // checkpoints, one before every group, so it has to scan in one direction only.
 //
@@ -18,14 +17,47 @@
 namespace ssm {
 
 constexpr unsigned kAll = 0xffffffffu;
+
+// 4-byte asynchronous copy global -> shared.
+__device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 constexpr int kGatedWarps = 4;  // warps of a block without SPLIT
 constexpr int kMaxSplit = 16;
 #ifndef FWD_MINB
-#define FWD_MINB 6
+#define FWD_MINB 4
+#endif
+#ifndef BWD_MINB32
+#define BWD_MINB32 3
 #endif
 #ifndef BWD_MINB
 #define BWD_MINB 4
 #endif
+
+// Dynamic shared memory of a block of the backward: the ring, and the checkpoints' slots.
+template <typename IO>
+constexpr int bwd_smem(bool gate, int threads) {
+    return kBwdStages<IO> * ((gate ? Ring<IO, kBwdSteps, 5>::kVecs : Ring<IO, kBwdSteps, 4>::kVecs) * 16 + 4) * threads;
+}
+
+// The product of a lane's decays, as join.
+template <bool CUT, int PAIRS>
+__device__ __forceinline__ float product(float2 (&a)[PAIRS]) {
+    if constexpr (CUT) {
+        float P = a[0].x;
+#pragma unroll
+        for (int e = 1; e < 2 * PAIRS; ++e) P = join<true>(P, step_of(a, e));
+        return P;
+    } else {
+        float2 q[PAIRS / 2];
+#pragma unroll
+        for (int k = 0; k < PAIRS / 2; ++k) q[k] = __fmul2_rn(a[2 * k], a[2 * k + 1]);
+#pragma unroll
+        for (int k = 1; k < PAIRS / 2; ++k) q[0] = __fmul2_rn(q[0], q[k]);
+        return q[0].x * q[0].y;
+    }
+}
 
 // The row of this lane, and where in it the lane works.
 template <int SEG, bool SPLIT>
@@ -59,7 +91,7 @@ __device__ __forceinline__ float join_parts(float2* pairs, int place, int parts,
 
 template <typename IO, bool GATE, bool RESET, int SEG, bool SPLIT>
 __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPLIT ? 1 : FWD_MINB) gated_fwd_kernel(const GatedParams p) {
-    constexpr int kStep = SEG * kGroup;
+    constexpr int N = kFwdSteps<IO>, kPairs = N / 2, kIn = 3;
     __shared__ float2 pairs[SPLIT ? 2 : 1][SPLIT ? kMaxSplit : 1];
     const RowPlace<SEG, SPLIT> at(p);
     const long long row = at.row;
@@ -68,12 +100,16 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     if (SEG == 32 && !valid) return;  // (a whole warp)
     const int b = valid ? static_cast<int>(row / p.dim) : 0, d = valid ? static_cast<int>(row % p.dim) : 0;
     const int len = valid ? row_length(p, b) : 0;
-    const IO *x = row_of<IO>(p.x, b, d), *r = row_of<IO>(p.r, b, d), *i = row_of<IO>(p.i, b, d);
-    const IO* z = GATE ? row_of<IO>(p.z, b, d) : nullptr;
+    const IO* in[kIn] = {row_of<IO>(p.x, b, d), row_of<IO>(p.r, b, d), row_of<IO>(p.i, b, d)};
+    const IO* zrow[1] = {GATE ? row_of<IO>(p.z, b, d) : nullptr};
     IO* y = p.y.p ? row_of<IO>(p.y, b, d) : nullptr;
-    const int phase = phase_of(x);
-    const bool vr = phase_of(r) == phase, vi = phase_of(i) == phase, vz = GATE && phase_of(z) == phase, vy = phase_of(y) == phase;
+    const int phase = phase_of(in[0]);
+    bool vec[kIn], all_vec = true;
+#pragma unroll
+    for (int k = 0; k < kIn; ++k) all_vec &= vec[k] = phase_of(in[k]) == phase;
+    const bool vy = phase_of(y) == phase, vz[1] = {phase_of(zrow[0]) == phase};
     const unsigned char* reset = RESET ? p.reset + static_cast<long long>(b) * p.L : nullptr;
+    const unsigned char* reset_end = RESET ? p.reset + static_cast<long long>(p.batch) * p.L : nullptr;
     const float rate = -p.c * softplus_lam(p.lam[d]);
     const bool near = rate > -kNear;
     const float rb = -kLog2e * (p.r_bias ? p.r_bias[d] : 0.f), ib = -kLog2e * (p.i_bias ? p.i_bias[d] : 0.f);
@@ -85,88 +121,109 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
                                                   static_cast<unsigned>(p.x.bs) % n, static_cast<unsigned>(p.x.ds) % n, 0};
     }
 
-    int t0 = (at.part * SEG + at.lane) * kGroup - phase;
-    const int stride = at.parts * kStep;
-    RawGroup<IO> nx = load_group(x, t0, len, p.L, true), nr = load_group(r, t0, len, p.L, vr), ni = load_group(i, t0, len, p.L, vi), nz;
-    if (GATE) nz = load_group(z, t0, len, p.L, vz);
+    constexpr bool kAhead = sizeof(IO) == 2 || F32_AHEAD;
+    int t0 = (at.part * SEG + at.lane) * N - phase;
+    const int stride = at.parts * SEG * N;
+    Raw<IO, N> next[kIn];
+    if (kAhead) load_steps(in, vec, all_vec, t0, valid ? p.L : 0, p.L, next);  // (not waiting for len)
     int round = 0;
 #pragma unroll 1
     for (int t = -phase; SEG == 32 ? t < len : __any_sync(kAll, t < len); t += stride, t0 += stride, ++round) {
         float2 a[kPairs], u[kPairs], v[kPairs], w[kPairs];
-        unpack<IO>(nx, u);
-        unpack<IO>(nr, v);
-        unpack<IO>(ni, w);
-        const RawGroup<IO> zc = nz;
-        // the next tile's loads are under way while this one is computed
-        nx = load_group(x, t0 + stride, len, p.L, true);
-        nr = load_group(r, t0 + stride, len, p.L, vr);
-        ni = load_group(i, t0 + stride, len, p.L, vi);
-        if (GATE) nz = load_group(z, t0 + stride, len, p.L, vz);
+        if (!kAhead) load_steps(in, vec, all_vec, t0, len, p.L, next);
+        unpack<IO, N>(next[0], u);
+        unpack<IO, N>(next[1], v);
+        unpack<IO, N>(next[2], w);
+        Raw<IO, N> zc[1];
+        if (GATE) load_steps(zrow, vz, vz[0], t0, len, p.L, zc);  // wanted last
+        if (kAhead) load_steps(in, vec, all_vec, t0 + stride, len, p.L, next);  // under way while this tile is computed
         const auto coefficients = [&](auto near_tag) {
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) {
                 const Gates gt = gates_of(v[k], w[k], rb, ib);
                 const Decay dec = decay_of<decltype(near_tag)::value>(__fmul2_rn(both(rate), gt.rho));
                 a[k] = dec.a;
-                v[k] = make_float2(sqrt_approx(dec.m2.x), sqrt_approx(dec.m2.y));
+                const float2 m = make_float2(sqrt_approx(dec.m2.x), sqrt_approx(dec.m2.y));
                 u[k] = __fmul2_rn(u[k], gt.iota);
+                if (RESET) v[k] = u[k];  // (m_t = 1 at a reset)
+                u[k] = __fmul2_rn(u[k], m);
             }
         };
         if (near)
             coefficients(std::true_type{});
         else
             coefficients(std::false_type{});
-        if (RESET && t0 < len) {
+        bool any_cut = false;
+        if (RESET) {
+            unsigned long long flags[N / 8], any = 0;
 #pragma unroll
-            for (int e = 0; e < kGroup; ++e)
-                if (t0 + e >= 0 && t0 + e < len && reset[t0 + e]) step_of(a, e) = kCut, step_of(v, e) = 1.f;
+            for (int k = 0; k < N / 8; ++k) any |= flags[k] = reset_flags(reset, t0 + 8 * k, len, p.reset, reset_end);
+            any_cut = __any_sync(kAll, any != 0);
+            if (any_cut) {
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if (flag_of(flags[e / 8], e % 8)) step_of(a, e) = kCut, step_of(u, e) = step_of(v, e);
+            }
         }
+        if (t0 < 0 || t0 + N > len) {
 #pragma unroll
-        for (int k = 0; k < kPairs; ++k) u[k] = __fmul2_rn(u[k], v[k]);
-        if (t0 < 0 || t0 + kGroup > len) {
-#pragma unroll
-            for (int e = 0; e < kGroup; ++e)
+            for (int e = 0; e < N; ++e)
                 if (t0 + e < 0 || t0 + e >= len) step_of(a, e) = 1.f, step_of(u, e) = 0.f;
         }
-        float P = a[0].x, H = u[0].x;
+        float P, H;
+        const auto compose = [&](auto cut_tag) {  // (P, H) of the tile up to and with this lane's steps
+            constexpr bool CUT = decltype(cut_tag)::value;
+            H = u[0].x;
 #pragma unroll
-        for (int e = 1; e < kGroup; ++e) {
-            H = carry_on<RESET>(step_of(a, e), H, step_of(u, e));
-            P = join<RESET>(P, step_of(a, e));
-        }
+            for (int e = 1; e < N; ++e) H = carry_on<CUT>(step_of(a, e), H, step_of(u, e));
+            P = product<CUT>(a);
 #pragma unroll
-        for (int s = 1; s < SEG; s *= 2) {
-            const float Pe = __shfl_up_sync(kAll, P, s, SEG), He = __shfl_up_sync(kAll, H, s, SEG);
-            if (at.lane >= s) H = carry_on<RESET>(P, He, H), P = join<RESET>(P, Pe);
+            for (int s = 1; s < SEG; s *= 2) {
+                const float Pe = __shfl_up_sync(kAll, P, s, SEG), He = __shfl_up_sync(kAll, H, s, SEG);
+                if (at.lane >= s) H = carry_on<CUT>(P, He, H), P = join<CUT>(P, Pe);
+            }
+        };
+        compose(std::false_type{});
+        bool careful = false;
+        if (RESET && any_cut) {
+            careful = __any_sync(kAll, !finite(H) || (!SPLIT && !finite(carry)));
+            if (careful) compose(std::true_type{});
         }
-        float h;
+        float enters = carry;
         if constexpr (SPLIT) {
-            const float in = join_parts<RESET>(pairs[round & 1], at.part, at.parts, at.lane == 31, P, H, carry);
-            const float all = carry_on<RESET>(P, in, H);
-            h = __shfl_up_sync(kAll, all, 1);
-            if (at.lane == 0) h = in;
-        } else {
-            const float all = carry_on<RESET>(P, carry, H);  // the state after this lane's steps
-            h = __shfl_up_sync(kAll, all, 1, SEG);
-            if (at.lane == 0) h = carry;
-            carry = __shfl_sync(kAll, all, SEG - 1, SEG);
+            enters = join_parts<RESET>(pairs[round & 1], at.part, at.parts, at.lane == 31, any_cut ? kCut : P, H, carry);
+            if (RESET && any_cut && !careful && !finite(enters)) careful = true, compose(std::true_type{});
         }
-        if (ckpt && t0 < len) ckpt[(t0 + phase) / kGroup] = h;
+        const auto states = [&](auto cut_tag) {
+            constexpr bool CUT = decltype(cut_tag)::value;
+            const float all = carry_on<CUT>(P, enters, H);  // the state after this lane's steps
+            float h = __shfl_up_sync(kAll, all, 1, SEG);
+            if (at.lane == 0) h = enters;
+            if (!SPLIT) carry = __shfl_sync(kAll, all, SEG - 1, SEG);
+            if (ckpt && t0 < len) ckpt[(t0 + phase) / kGroup] = h;
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e) step_of(u, e) = h = carry_on<RESET>(step_of(a, e), h, step_of(u, e));
+            for (int e = 0; e < N; ++e) {
+                if (e == kGroup && ckpt && t0 + kGroup < len) ckpt[(t0 + phase) / kGroup + 1] = h;
+                step_of(u, e) = h = carry_on<CUT>(step_of(a, e), h, step_of(u, e));
+            }
+        };
+        if (RESET && careful)
+            states(std::true_type{});
+        else
+            states(std::false_type{});
         if (GATE) {
-            unpack<IO>(zc, w);
+            unpack<IO, N>(zc[0], w);
 #pragma unroll
-            for (int k = 0; k < kPairs; ++k) u[k] = __fmul2_rn(u[k], __fmul2_rn(w[k], sigmoid2(w[k])));
+            for (int k = 0; k < kPairs; ++k) u[k] = __fmul2_rn(u[k], gate_silu2<IO>(w[k]));
         }
-        if (y) store_group(y, t0, len, vy, u);
+        if (y) store_steps(y, t0, len, vy, u);
     }
     if (p.last && valid && at.part == 0 && at.lane == 0) p.last[row] = carry;
 }
 
 template <typename IO, bool GATE, bool RESET, int SEG, bool SPLIT>
-__global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPLIT ? 1 : BWD_MINB) gated_bwd_kernel(const GatedParams p) {
-    constexpr int kStep = SEG * kGroup;
+__global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPLIT ? 1 : (sizeof(IO) == 2 ? BWD_MINB : BWD_MINB32)) gated_bwd_kernel(const GatedParams p) {
+    constexpr int N = kBwdSteps, kPairs = N / 2, kIn = GATE ? 5 : 4, kOut = GATE ? 4 : 3;
     __shared__ float2 pairs[SPLIT ? 2 : 1][SPLIT ? kMaxSplit : 1];
     __shared__ float part_sums[SPLIT ? 3 : 1][SPLIT ? kMaxSplit : 1];
     const RowPlace<SEG, SPLIT> at(p);
@@ -176,16 +233,18 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     if (SEG == 32 && !valid) return;
     const int b = valid ? static_cast<int>(row / p.dim) : 0, d = valid ? static_cast<int>(row % p.dim) : 0;
     const int len = valid ? row_length(p, b) : 0, L = valid ? p.L : 0;
-    const IO *x = row_of<IO>(p.x, b, d), *r = row_of<IO>(p.r, b, d), *i = row_of<IO>(p.i, b, d);
-    const IO *z = GATE ? row_of<IO>(p.z, b, d) : nullptr, *dy = row_of<IO>(p.dy, b, d);
-    IO *dx = row_of<IO>(p.dx, b, d), *dr = row_of<IO>(p.dr, b, d), *di = row_of<IO>(p.di, b, d);
-    IO* dz = GATE ? row_of<IO>(p.dz, b, d) : nullptr;
+    const IO* in[kIn] = {row_of<IO>(p.x, b, d), row_of<IO>(p.r, b, d), row_of<IO>(p.i, b, d), row_of<IO>(p.dy, b, d)};
+    IO* out[kOut] = {row_of<IO>(p.dx, b, d), row_of<IO>(p.dr, b, d), row_of<IO>(p.di, b, d)};
+    if (GATE) in[kIn - 1] = row_of<IO>(p.z, b, d), out[kOut - 1] = row_of<IO>(p.dz, b, d);
     const CkptHeader where = *reinterpret_cast<const CkptHeader*>(p.ckpt);
     const int phase = static_cast<int>((where.base + b * where.bs + d * where.ds) % (16 / sizeof(IO)));
-    const bool vx = phase_of(x) == phase, vr = phase_of(r) == phase, vi = phase_of(i) == phase, vz = GATE && phase_of(z) == phase,
-               vdy = phase_of(dy) == phase, vdx = phase_of(dx) == phase, vdr = phase_of(dr) == phase, vdi = phase_of(di) == phase,
-               vdz = GATE && phase_of(dz) == phase;
+    bool vin[kIn], vout[kOut], all_vec = true;
+#pragma unroll
+    for (int k = 0; k < kIn; ++k) all_vec &= vin[k] = phase_of(in[k]) == phase;
+#pragma unroll
+    for (int k = 0; k < kOut; ++k) all_vec &= vout[k] = phase_of(out[k]) == phase;
     const unsigned char* reset = RESET ? p.reset + static_cast<long long>(b) * p.L : nullptr;
+    const unsigned char* reset_end = RESET ? p.reset + static_cast<long long>(p.batch) * p.L : nullptr;
     const float* ckpt = p.ckpt + sizeof(CkptHeader) / 4 + row * p.ckpt_row;
     const float rate = -p.c * softplus_lam(p.lam[d]);
     const bool near = rate > -kNear;
@@ -193,35 +252,60 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     float carry = p.dlast && valid ? p.dlast[row] : 0.f;  // a_{t+1} g_{t+1}: what the steps after the tile send back
     float2 sumT = both(0.f), sumr = both(0.f), sumi = both(0.f);
 
-    const int stride = at.parts * kStep;
+    const int stride = at.parts * SEG * N;
     int t = (len + phase + stride - 1) / stride * stride - phase;  // where the rounds with steps end
-    for (int t0 = t + (at.part * SEG + at.lane) * kGroup; t0 < L; t0 += stride) {  // padding: zeros
+    for (int t0 = t + (at.part * SEG + at.lane) * N; t0 < L; t0 += stride) {  // padding: zeros
         float2 zero[kPairs] = {};
-        store_group(dx, t0, L, vdx, zero);
-        store_group(dr, t0, L, vdr, zero);
-        store_group(di, t0, L, vdi, zero);
-        if (GATE) store_group(dz, t0, L, vdz, zero);
+#pragma unroll
+        for (int k = 0; k < kOut; ++k) store_steps(out[k], t0, L, vout[k], zero);
     }
-    int round = 0;
+    using In = Ring<IO, N, kIn>;
+    constexpr int kStages = kBwdStages<IO>;
+    extern __shared__ uint4 ring[];
+    float* states_in = reinterpret_cast<float*>(ring + kStages * In::kVecs * blockDim.x) + threadIdx.x;  // the checkpoints' slots
+    const auto load = [&](int stage, int t) {
+        const int t0 = t + (at.part * SEG + at.lane) * N;
+        const bool active = t >= -phase;
+        if (active && t0 < len) cp_async_4(states_in + stage * blockDim.x, ckpt + (t0 + phase) / kGroup);
+        In::load(ring, stage, in, vin, all_vec, t0, active ? len : -N, p.L);
+    };
+    int round = 0, stage = 0;
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) load(k, t - (k + 1) * stride);
 #pragma unroll 1
     for (t -= stride; SEG == 32 ? t >= -phase : __any_sync(kAll, t >= -phase); t -= stride, ++round) {
-        const int t0 = t + (at.part * SEG + at.lane) * kGroup;
-        // (a short row that is done while others of its warp go on: t0 below its first step, no steps inside)
-        const int end = t >= -phase ? len : -phase;
+        const int t0 = t + (at.part * SEG + at.lane) * N;
+        // (a short row that is done while others of its warp go on lies before its first step: no steps inside)
+        const bool active = SEG == 32 || t >= -phase;
+        const int end = active ? len : -phase;
+        const bool whole = t0 >= 0 && t0 + N <= end;
         float2 a[kPairs], g[kPairs], kx[kPairs], ki[kPairs], kT[kPairs], kr[kPairs], b[kPairs], ax[kPairs];
-        const RawGroup<IO> rz = GATE ? load_group(z, t0, end, p.L, vz) : RawGroup<IO>{};
-        {
-            const RawGroup<IO> rx = load_group(x, t0, end, p.L, vx), rr = load_group(r, t0, end, p.L, vr),
-                               ri = load_group(i, t0, end, p.L, vi), rg = load_group(dy, t0, end, p.L, vdy);
-            unpack<IO>(rx, kx);
-            unpack<IO>(rr, kr);
-            unpack<IO>(ri, ki);
-            unpack<IO>(rg, g);
+        Raw<IO, N> raw[kIn];
+        float h = 0.f;
+        if constexpr (kStages > 0) {
+            cp_async_wait<kStages - 2>();
+#pragma unroll
+            for (int k = 0; k < kIn; ++k) raw[k] = In::read(ring, stage, k);
+            if (t0 < end && active) h = states_in[stage * blockDim.x];
+            load(stage == 0 ? kStages - 1 : stage - 1, t - (kStages - 1) * stride);
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+        } else {
+            if (t0 < end && active) h = ckpt[(t0 + phase) / kGroup];
+            load_steps(in, vin, all_vec, t0, active ? end : -N, p.L, raw);
         }
-        float h = t0 >= -phase && t0 < end ? ckpt[(t0 + phase) / kGroup] : 0.f;
+        unpack<IO, N>(raw[0], kx);
+        unpack<IO, N>(raw[1], kr);
+        unpack<IO, N>(raw[2], ki);
+        unpack<IO, N>(raw[3], g);
+        bool any_cut = false;
+        unsigned long long flags = 0;
+        if (RESET) {
+            flags = reset_flags(reset, t0, end, p.reset, reset_end);
+            any_cut = __any_sync(kAll, flags != 0);
+        }
         // what g_t is to be multiplied by, for each gradient:
         //   dx  kx = m iota         di  ki = b (1 - iota), b = m iota x
-        //   T   kT = a (iota x a v / m - h_{t-1} v), its first part here      dr  T kr, kr = 1 - rho
+        //   T = a (iota x a v / m - h_{t-1} v) = h_{t-1} ax - kT       dr  T kr, kr = 1 - rho
         const auto coefficients = [&](auto near_tag) {
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) {
@@ -230,89 +314,120 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
                 const Decay dec = decay_of<decltype(near_tag)::value>(xv);
                 // v -> 0: m and v / m go to 0
                 const float2 rs = make_float2(rsqrt_approx(fmaxf(dec.m2.x, 1e-30f)), rsqrt_approx(fmaxf(dec.m2.y, 1e-30f)));
-                const float2 ux = __fmul2_rn(gt.iota, kx[k]), m = __fmul2_rn(dec.m2, rs);
+                const float2 ux = __fmul2_rn(gt.iota, kx[k]);
+                float2 m = __fmul2_rn(dec.m2, rs);
                 a[k] = dec.a;
                 ax[k] = __fmul2_rn(dec.a, xv);
-                kT[k] = __fmul2_rn(__fmul2_rn(make_float2(-dec.a.x, -dec.a.y), __fmul2_rn(ax[k], rs)), ux);
+                kT[k] = __fmul2_rn(__fmul2_rn(ax[k], dec.a), __fmul2_rn(rs, ux));
                 kr[k] = __fmul2_rn(gt.Er, gt.rho);
+                if (RESET && any_cut) {
+                    if (flag_of(flags, 2 * k)) a[k].x = kCut, m.x = 1.f, ax[k].x = kT[k].x = 0.f;
+                    if (flag_of(flags, 2 * k + 1)) a[k].y = kCut, m.y = 1.f, ax[k].y = kT[k].y = 0.f;
+                }
                 kx[k] = __fmul2_rn(m, gt.iota);
                 b[k] = __fmul2_rn(m, ux);
                 ki[k] = __fmul2_rn(b[k], __fmul2_rn(gt.Ei, gt.iota));
-                if constexpr (RESET) {
-                    const int t = t0 + 2 * k;
-                    const bool c0 = t >= 0 && t < end && reset[t], c1 = t + 1 >= 0 && t + 1 < end && reset[t + 1];
-                    if (c0) a[k].x = kCut, ax[k].x = kT[k].x = 0.f, kx[k].x = gt.iota.x, b[k].x = ux.x, ki[k].x = ux.x * (gt.Ei.x * gt.iota.x);
-                    if (c1) a[k].y = kCut, ax[k].y = kT[k].y = 0.f, kx[k].y = gt.iota.y, b[k].y = ux.y, ki[k].y = ux.y * (gt.Ei.y * gt.iota.y);
-                }
             }
         };
         if (near)
             coefficients(std::true_type{});
         else
             coefficients(std::false_type{});
-        const bool whole = t0 >= 0 && t0 + kGroup <= end;
         if (!whole) {
 #pragma unroll
-            for (int e = 0; e < kGroup; ++e)
+            for (int e = 0; e < N; ++e)
                 if (t0 + e < 0 || t0 + e >= end) {
                     step_of(a, e) = 1.f;
                     step_of(g, e) = step_of(kT, e) = step_of(ax, e) = step_of(kr, e) = step_of(ki, e) = step_of(kx, e) = step_of(b, e) = 0.f;
                 }
         }
+        const auto states = [&](auto cut_tag) {
+            constexpr bool CUT = decltype(cut_tag)::value;
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e) {  // b becomes the states
-            const float term = fmaf(h, step_of(ax, e), step_of(kT, e));
-            step_of(kT, e) = RESET && is_cut(step_of(a, e)) ? 0.f : term;
-            step_of(b, e) = h = carry_on<RESET>(step_of(a, e), h, step_of(b, e));
+            for (int e = 0; e < N; ++e) {  // kT becomes T, b the states
+                const float term = fmaf(h, step_of(ax, e), -step_of(kT, e));
+                step_of(kT, e) = CUT && is_cut(step_of(a, e)) ? 0.f : term;
+                step_of(b, e) = h = carry_on<CUT>(step_of(a, e), h, step_of(b, e));
+            }
+        };
+        bool careful = false;
+        if (RESET && any_cut) {  // no state is larger than this sum
+            float most = fabsf(h);
+#pragma unroll
+            for (int e = 0; e < N; ++e) most += fabsf(step_of(b, e));
+            careful = __any_sync(kAll, !finite(most));
         }
+        if (RESET && careful)
+            states(std::true_type{});
+        else
+            states(std::false_type{});
         if (GATE) {
             float2 zv[kPairs];
-            unpack<IO>(rz, zv);
+            unpack<IO, N>(raw[kIn - 1], zv);
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) {
                 const float2 sig = sigmoid2(zv[k]), zs = __fmul2_rn(zv[k], sig);
-                // silu' = sig (1 + z (1 - sig)) = sig + z sig - z sig sig
-                const float2 slope = __ffma2_rn(make_float2(-zs.x, -zs.y), sig, __fadd2_rn(sig, zs));
+                // silu' = sig + z sig (1 - sig)
+                const float2 slope = __ffma2_rn(zs, __ffma2_rn(both(-1.f), sig, both(1.f)), sig);
                 b[k] = __fmul2_rn(__fmul2_rn(g[k], b[k]), slope);
                 g[k] = __fmul2_rn(g[k], zs);
             }
-            if (!whole) {
+            if (all_vec && whole) {
+                store_vectors(out[kOut - 1], t0, b);
+            } else {
 #pragma unroll
-                for (int e = 0; e < kGroup; ++e)
+                for (int e = 0; e < N; ++e)
                     if (t0 + e < 0 || t0 + e >= end) step_of(g, e) = step_of(b, e) = 0.f;
+                if (active) store_steps(out[kOut - 1], t0, L, vout[kOut - 1], b);
             }
-            if (t >= -phase) store_group(dz, t0, L, vdz, b);
         }
-        float P = 1.f, S = 0.f;
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) ax[k] = __fmul2_rn(a[k], g[k]);
+        float P, S;
+        const auto compose = [&](auto cut_tag) {  // (P, S) of the tile from this lane's steps on
+            constexpr bool CUT = decltype(cut_tag)::value;
+            S = ax[kPairs - 1].y;
 #pragma unroll
-        for (int e = kGroup - 1; e >= 0; --e) {
-            S = carry_on<RESET>(step_of(a, e), S, step_of(ax, e));
-            P = join<RESET>(P, step_of(a, e));
-        }
+            for (int e = N - 2; e >= 0; --e) S = carry_on<CUT>(step_of(a, e), S, step_of(ax, e));
+            P = product<CUT>(a);
 #pragma unroll
-        for (int s = 1; s < SEG; s *= 2) {
-            const float Pl = __shfl_down_sync(kAll, P, s, SEG), Sl = __shfl_down_sync(kAll, S, s, SEG);
-            if (at.lane + s < SEG) S = carry_on<RESET>(P, Sl, S), P = join<RESET>(P, Pl);
+            for (int s = 1; s < SEG; s *= 2) {
+                const float Pl = __shfl_down_sync(kAll, P, s, SEG), Sl = __shfl_down_sync(kAll, S, s, SEG);
+                if (at.lane + s < SEG) S = carry_on<CUT>(P, Sl, S), P = join<CUT>(P, Pl);
+            }
+        };
+        const auto drop = [&] {  // a reset's own gradient goes nowhere either, not even as 0 * inf
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (is_cut(step_of(a, e))) step_of(ax, e) = 0.f;
+        };
+        compose(std::false_type{});
+        careful = false;
+        if (RESET && any_cut) {
+            careful = __any_sync(kAll, !finite(S) || (!SPLIT && !finite(carry)));
+            if (careful) drop(), compose(std::true_type{});
         }
-        float s;
+        float enters = carry;
         if constexpr (SPLIT) {
-            const float in = join_parts<RESET>(pairs[round & 1], at.parts - 1 - at.part, at.parts, at.lane == 0, P, S, carry);
-            const float all = carry_on<RESET>(P, in, S);
-            s = __shfl_down_sync(kAll, all, 1);
-            if (at.lane == 31) s = in;
-        } else {
-            const float all = carry_on<RESET>(P, carry, S);
-            s = __shfl_down_sync(kAll, all, 1, SEG);
-            if (at.lane == SEG - 1) s = carry;
-            carry = __shfl_sync(kAll, all, 0, SEG);
+            enters = join_parts<RESET>(pairs[round & 1], at.parts - 1 - at.part, at.parts, at.lane == 0, any_cut ? kCut : P, S, carry);
+            if (RESET && any_cut && !careful && !finite(enters)) careful = true, drop(), compose(std::true_type{});
         }
+        const auto gradients = [&](auto cut_tag) {
+            constexpr bool CUT = decltype(cut_tag)::value;
+            const float all = carry_on<CUT>(P, enters, S);
+            float s = __shfl_down_sync(kAll, all, 1, SEG);
+            if (at.lane == SEG - 1) s = enters;
+            if (!SPLIT) carry = __shfl_sync(kAll, all, 0, SEG);
 #pragma unroll
-        for (int e = kGroup - 1; e >= 0; --e) {
-            step_of(g, e) += s;
-            s = carry_on<RESET>(step_of(a, e), s, step_of(ax, e));
-        }
+            for (int e = N - 1; e >= 0; --e) {
+                step_of(g, e) += s;
+                s = carry_on<CUT>(step_of(a, e), s, step_of(ax, e));
+            }
+        };
+        if (RESET && careful)
+            gradients(std::true_type{});
+        else
+            gradients(std::false_type{});
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) {
             const float2 T = __fmul2_rn(g[k], kT[k]);
@@ -323,15 +438,17 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
             sumr = __fadd2_rn(sumr, kr[k]);
             sumi = __fadd2_rn(sumi, ki[k]);
         }
-        if (!whole) {  // (0 times an infinite gradient of the last state)
+        if (all_vec && whole) {
+            store_vectors(out[0], t0, kx);
+            store_vectors(out[1], t0, kr);
+            store_vectors(out[2], t0, ki);
+        } else if (active) {
 #pragma unroll
-            for (int e = 0; e < kGroup; ++e)
+            for (int e = 0; e < N; ++e)  // (0 times an infinite gradient of the last state)
                 if (t0 + e >= end) step_of(kx, e) = step_of(kr, e) = step_of(ki, e) = 0.f;
-        }
-        if (t >= -phase) {
-            store_group(dx, t0, L, vdx, kx);
-            store_group(dr, t0, L, vdr, kr);
-            store_group(di, t0, L, vdi, ki);
+            store_steps(out[0], t0, L, vout[0], kx);
+            store_steps(out[1], t0, L, vout[1], kr);
+            store_steps(out[2], t0, L, vout[2], ki);
         }
     }
     if (p.dh0 && valid && at.part == 0 && at.lane == 0) p.dh0[row] = carry;
