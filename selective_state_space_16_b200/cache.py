@@ -6,9 +6,8 @@ import struct
 
 import torch
 
-from . import binding
 from .binding import _check
-from .gated import _buffer, _call, _dense
+from .gated import _buffer, _call, _dense, _lib
 
 SSM_CACHE_NEW = -1  # as a parent: the page of a new sequence, all zeros
 MAX_POOLS = 8
@@ -53,17 +52,18 @@ class CachePools:
             e = t.element_size()
             packed.append(_POOL.pack(t.data_ptr(), dense * e, t.stride(1) * e, t.stride(0) * e, t.shape[0]))
         self.tensors, self.n_slots, self.device = tensors, tensors[0].shape[1], tensors[0].device
+        self.index = tensors[0].get_device()
         self.packed, self.n_pools = b"".join(packed), len(tensors)
 
 
 def _list(t, name, pools):
     if t is None or t.dim() != 1:
         raise ValueError(f"{name}: expected a list of slots (int32, one dimension)")
-    return _dense(t, name, t.shape, _I32, pools.device)
+    return _dense(t, name, t.shape, _I32, pools.index)
 
 
 def ssm_cache_workspace_size(n_slots: int, n: int) -> int:
-    return int(binding.load().ssm_cache_workspace_size(n_slots, n))
+    return int(_lib().ssm_cache_workspace_size(n_slots, n))
 
 
 def new_cache_workspace(pools, n=0, device=None):
@@ -76,8 +76,8 @@ def ssm_cache_copy(pools, src, dst, workspace, stream=None, check=True):
     a, b = _list(src, "src", pools), _list(dst, "dst", pools)
     if src.shape != dst.shape:
         raise ValueError(f"{src.numel()} sources, {dst.numel()} destinations")
-    code = _call(pools, stream, binding.load().ssm_cache_copy, pools.packed, pools.n_pools, pools.n_slots, a, b, src.numel(),
-                 _buffer(workspace, "workspace", 0, pools.device), workspace.numel() * workspace.element_size())
+    code = _call(pools.index, stream, _lib().ssm_cache_copy, pools.packed, pools.n_pools, pools.n_slots, a, b, src.numel(),
+                 _buffer(workspace, "workspace", 0, pools.index), workspace.nbytes)
     if check:
         _check(code, "ssm_cache_copy")
     return code
@@ -89,9 +89,9 @@ def ssm_cache_fork(pools, used, parents, children, workspace, stream=None, check
     a, b = _list(parents, "parents", pools), _list(children, "children", pools)
     if parents.shape != children.shape:
         raise ValueError(f"{parents.numel()} parents, {children.numel()} children")
-    code = _call(pools, stream, binding.load().ssm_cache_fork, pools.packed, pools.n_pools, pools.n_slots,
-                 _dense(used, "used", (pools.n_slots,), _I32, pools.device), a, b, parents.numel(),
-                 _buffer(workspace, "workspace", 0, pools.device), workspace.numel() * workspace.element_size())
+    code = _call(pools.index, stream, _lib().ssm_cache_fork, pools.packed, pools.n_pools, pools.n_slots,
+                 _dense(used, "used", (pools.n_slots,), _I32, pools.index), a, b, parents.numel(),
+                 _buffer(workspace, "workspace", 0, pools.index), workspace.nbytes)
     if check:
         _check(code, "ssm_cache_fork")
     return code
@@ -100,8 +100,8 @@ def ssm_cache_fork(pools, used, parents, children, workspace, stream=None, check
 def ssm_cache_free(pools, used, slots, zero_pages=False, stream=None, check=True):
     """Free the listed slots (used = 0), with zero_pages also clearing their pages."""
     a = _list(slots, "slots", pools)
-    code = _call(pools, stream, binding.load().ssm_cache_free, pools.packed, pools.n_pools, pools.n_slots,
-                 _dense(used, "used", (pools.n_slots,), _I32, pools.device), a, slots.numel(), int(bool(zero_pages)))
+    code = _call(pools.index, stream, _lib().ssm_cache_free, pools.packed, pools.n_pools, pools.n_slots,
+                 _dense(used, "used", (pools.n_slots,), _I32, pools.index), a, slots.numel(), int(bool(zero_pages)))
     if check:
         _check(code, "ssm_cache_free")
     return code
@@ -110,11 +110,11 @@ def ssm_cache_free(pools, used, slots, zero_pages=False, stream=None, check=True
 def ssm_cache_compact(pools, used, table, remap, count, workspace, stream=None, check=True):
     """Move the used pages to the front.  used: (slots) int32 in/out; table: (n) int32 slots that follow their pages,
     or None; remap: (slots) int32 output or None; count: (1) int32 output or None."""
-    code = _call(pools, stream, binding.load().ssm_cache_compact, pools.packed, pools.n_pools, pools.n_slots,
-                 _dense(used, "used", (pools.n_slots,), _I32, pools.device), 0 if table is None else _list(table, "table", pools),
-                 0 if table is None else table.numel(), _dense(remap, "remap", (pools.n_slots,), _I32, pools.device),
-                 _dense(count, "count", (1,), _I32, pools.device), _buffer(workspace, "workspace", 0, pools.device),
-                 workspace.numel() * workspace.element_size())
+    code = _call(pools.index, stream, _lib().ssm_cache_compact, pools.packed, pools.n_pools, pools.n_slots,
+                 _dense(used, "used", (pools.n_slots,), _I32, pools.index), 0 if table is None else _list(table, "table", pools),
+                 0 if table is None else table.numel(), _dense(remap, "remap", (pools.n_slots,), _I32, pools.index),
+                 _dense(count, "count", (1,), _I32, pools.index), _buffer(workspace, "workspace", 0, pools.index),
+                 workspace.nbytes)
     if check:
         _check(code, "ssm_cache_compact")
     return code

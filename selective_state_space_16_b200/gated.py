@@ -43,18 +43,26 @@ def declare(lib: ctypes.CDLL) -> None:
 
 _IO = {torch.bfloat16: SSM_BF16, torch.float32: SSM_F32}
 
+# The current stream's handle and the current device without building torch's objects for them, which
+# takes longer than the rest of a call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
-def _call(tensor, stream, fn, *args):
-    """fn(*args, stream) with the tensor's device current."""
-    dev = tensor.device
-    if stream is not None:
-        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+def _call(dev, stream, fn, *args):
+    """fn(*args, stream) with device `dev` (an index) current."""
+    if stream is None:
+        raw = _raw_stream(dev)
     else:
-        raw = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if dev == _current_device():
         return fn(*args, raw)
     with torch.cuda.device(dev):
         return fn(*args, raw)
+
+
+def _lib():
+    return binding._lib or binding.load()
 
 
 @contextlib.contextmanager
@@ -74,15 +82,15 @@ def _allocating(tensor, stream):
 
 
 def _dense(t, name, shape, dtypes, dev):
-    """Address of an optional dense tensor."""
+    """Address of an optional dense tensor on device `dev` (an index)."""
     if t is None:
         return 0
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: {t.dtype} (expected {' or '.join(str(d) for d in dtypes)})")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected a dense tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
     return t.data_ptr()
 
 
@@ -91,57 +99,70 @@ _I32 = (torch.int32,)
 _FLAG = (torch.uint8, torch.bool)
 
 
-def _seq(t, name, like):
+def _like(t, name, x, dtype, shape, dev):
+    """Address of an operand of x's type and shape."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: {t.dtype} (x is {dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} (x has {tuple(shape)})")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, x on {x.device}")
+    return t.data_ptr()
+
+
+def _seq(t, name, x, dtype, shape, dev):
     """Address, batch stride and dim stride of a (batch, dim, seqlen) operand."""
     if t is None:
         return 0, 0, 0
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name}: {t.dtype} (x is {like.dtype})")
-    if t.shape != like.shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} (x has {tuple(like.shape)})")
+    at = _like(t, name, x, dtype, shape, dev)
     sb, sd, sl = t.stride()
-    if sl != 1 and t.shape[2] > 1:
+    if sl != 1 and shape[2] > 1:
         raise ValueError(f"{name}: consecutive steps must be next to each other (stride {sl})")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, x on {like.device}")
-    return t.data_ptr(), sb, sd
+    return at, sb, sd
 
 
-def _args(x, r, i, lam, r_bias, i_bias, z, initial_state, lengths, reset, c):
-    io = _IO.get(x.dtype)
+def _io(x, dims):
+    """io_dtype, dtype, shape and device index of the leading operand."""
+    dtype = x.dtype
+    io = _IO.get(dtype)
     if io is None:
-        raise TypeError(f"unsupported I/O dtype {x.dtype}")
-    if x.dim() != 3:
-        raise ValueError(f"x: expected (batch, dim, seqlen), got {tuple(x.shape)}")
-    if not x.is_cuda:
+        raise TypeError(f"unsupported I/O dtype {dtype}")
+    dev, shape = x.get_device(), x.shape
+    if dev < 0:
         raise ValueError("x: not a CUDA tensor")
-    b, d, L = x.shape
-    dev = x.device
+    if len(shape) != dims:
+        raise ValueError(f"x: expected {'(batch, dim, seqlen)' if dims == 3 else '(batch, dim)'}, got {tuple(shape)}")
+    return io, dtype, shape, dev
+
+
+def _args(like, r, i, lam, r_bias, i_bias, z, initial_state, lengths, reset, c):
+    x, dtype, shape, dev, io = like
     if lam is None:
         raise ValueError("lam is required")
-    ch, rows = (d,), (b, d)
-    return _ARGS.pack(*_seq(x, "x", x), *_seq(r, "r", x), *_seq(i, "i", x), *_seq(z, "z", x),
-                      _dense(lam, "lam", ch, _F32, dev), _dense(r_bias, "r_bias", ch, _F32, dev),
-                      _dense(i_bias, "i_bias", ch, _F32, dev), _dense(initial_state, "initial_state", rows, _F32, dev),
+    b, d, L = shape
+    ch = (d,)
+    return _ARGS.pack(*_seq(x, "x", x, dtype, shape, dev), *_seq(r, "r", x, dtype, shape, dev), *_seq(i, "i", x, dtype, shape, dev),
+                      *_seq(z, "z", x, dtype, shape, dev), _dense(lam, "lam", ch, _F32, dev), _dense(r_bias, "r_bias", ch, _F32, dev),
+                      _dense(i_bias, "i_bias", ch, _F32, dev), _dense(initial_state, "initial_state", (b, d), _F32, dev),
                       _dense(lengths, "lengths", (b,), _I32, dev), _dense(reset, "reset", (b, L), _FLAG, dev), L, b, d, io, c)
 
 
 def _buffer(t, name, bytes_, dev):
     if t is None:
         return 0
-    if not t.is_contiguous() or t.device != dev:
-        raise ValueError(f"{name}: expected a dense tensor on {dev}")
-    if t.numel() * t.element_size() < bytes_:
-        raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes, {bytes_} needed")
+    if not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: expected a dense tensor on cuda:{dev}")
+    if t.nbytes < bytes_:
+        raise ValueError(f"{name}: {t.nbytes} bytes, {bytes_} needed")
     return t.data_ptr()
 
 
 def ssm_gated_checkpoint_size(batch: int, dim: int, seqlen: int) -> int:
-    return int(binding.load().ssm_gated_checkpoint_size(batch, dim, seqlen))
+    return int(_lib().ssm_gated_checkpoint_size(batch, dim, seqlen))
 
 
 def ssm_gated_bwd_workspace_size(batch: int, dim: int, seqlen: int, have_checkpoints: bool = False) -> int:
-    return int(binding.load().ssm_gated_bwd_workspace_size(batch, dim, seqlen, int(bool(have_checkpoints))))
+    return int(_lib().ssm_gated_bwd_workspace_size(batch, dim, seqlen, int(bool(have_checkpoints))))
 
 
 def new_gated_checkpoints(batch, dim, seqlen, device="cuda"):
@@ -160,12 +181,13 @@ def ssm_gated_scan_fwd(x, r, i, lam, r_bias, i_bias, z, y, last_state, initial_s
     """Marshal a forward call.  x/r/i/z/y: (b, d, L), any batch and channel strides; lam/r_bias/i_bias: (d)
     fp32 (biases may be None); z may be None; last_state/initial_state: (b, d) fp32 or None; lengths: (b)
     int32 or None; reset: (b, L) uint8 or bool or None; checkpoints: from new_gated_checkpoints, or None."""
-    args = _args(x, r, i, lam, r_bias, i_bias, z, initial_state, lengths, reset, c)
-    b, d, L = x.shape
-    dev = x.device
-    ck = 0 if checkpoints is None else _buffer(checkpoints, "checkpoints", ssm_gated_checkpoint_size(b, d, L), dev)
-    code = _call(x, stream, binding.load().ssm_gated_scan_fwd, args, GatedOut(*_seq(y, "y", x)),
-                 _dense(last_state, "last_state", (b, d), _F32, dev), ck)
+    io, dtype, shape, dev = _io(x, 3)
+    args = _args((x, dtype, shape, dev, io), r, i, lam, r_bias, i_bias, z, initial_state, lengths, reset, c)
+    if y is None:
+        raise ValueError("y is required")
+    ck = 0 if checkpoints is None else _buffer(checkpoints, "checkpoints", ssm_gated_checkpoint_size(*shape), dev)
+    code = _call(dev, stream, _lib().ssm_gated_scan_fwd, args, GatedOut(*_seq(y, "y", x, dtype, shape, dev)),
+                 _dense(last_state, "last_state", shape[:2], _F32, dev), ck)
     if check:
         _check(code, "ssm_gated_scan_fwd")
     return code
@@ -176,16 +198,17 @@ def ssm_gated_scan_bwd(x, r, i, lam, r_bias, i_bias, z, dy, dx, dr, di, dlam, dr
                        checkpoints=None, c=8.0, stream=None, check=True):
     """Marshal a backward call (shapes as the forward; dlam/dr_bias/di_bias (d) fp32 or None, dinitial_state
     (b, d) fp32 or None; dz required with z; checkpoints: the forward's, or None)."""
-    args = _args(x, r, i, lam, r_bias, i_bias, z, initial_state, lengths, reset, c)
-    b, d, L = x.shape
-    dev, ch, rows = x.device, (d,), (b, d)
-    grads = _GRADS.pack(*_seq(dy, "dy", x), _dense(dlast_state, "dlast_state", rows, _F32, dev), *_seq(dx, "dx", x),
-                        *_seq(dr, "dr", x), *_seq(di, "di", x), *_seq(dz, "dz", x), _dense(dlam, "dlam", ch, _F32, dev),
+    io, dtype, shape, dev = _io(x, 3)
+    like = (x, dtype, shape, dev)
+    args = _args((*like, io), r, i, lam, r_bias, i_bias, z, initial_state, lengths, reset, c)
+    ch, rows = (shape[1],), shape[:2]
+    grads = _GRADS.pack(*_seq(dy, "dy", *like), _dense(dlast_state, "dlast_state", rows, _F32, dev), *_seq(dx, "dx", *like),
+                        *_seq(dr, "dr", *like), *_seq(di, "di", *like), *_seq(dz, "dz", *like), _dense(dlam, "dlam", ch, _F32, dev),
                         _dense(dr_bias, "dr_bias", ch, _F32, dev), _dense(di_bias, "di_bias", ch, _F32, dev),
                         _dense(dinitial_state, "dinitial_state", rows, _F32, dev))
-    ck = 0 if checkpoints is None else _buffer(checkpoints, "checkpoints", ssm_gated_checkpoint_size(b, d, L), dev)
-    code = _call(x, stream, binding.load().ssm_gated_scan_bwd, args, grads, ck, _buffer(workspace, "workspace", 0, dev),
-                 0 if workspace is None else workspace.numel() * workspace.element_size())
+    ck = 0 if checkpoints is None else _buffer(checkpoints, "checkpoints", ssm_gated_checkpoint_size(*shape), dev)
+    code = _call(dev, stream, _lib().ssm_gated_scan_bwd, args, grads, ck, _buffer(workspace, "workspace", 0, dev),
+                 0 if workspace is None else workspace.nbytes)
     if check:
         _check(code, "ssm_gated_scan_bwd")
     return code
@@ -194,37 +217,24 @@ def ssm_gated_scan_bwd(x, r, i, lam, r_bias, i_bias, z, dy, dx, dr, di, dlam, dr
 def ssm_gated_state_update(state, x, r, i, lam, r_bias, i_bias, z, y, slots=None, c=8.0, stream=None, check=True):
     """Marshal a one-token step.  state: (slots, d) fp32 in/out, rows of any stride; x/r/i/z/y: (b, d), rows of
     any stride; slots: (b) int32, the state of each row (outside the pool: the row is skipped), or None."""
-    io = _IO.get(x.dtype)
-    if io is None:
-        raise TypeError(f"unsupported I/O dtype {x.dtype}")
-    if not x.is_cuda:
-        raise ValueError("x: not a CUDA tensor")
-    b, d = x.shape
-    dev = x.device
-    at = []
-    for name, t in (("x", x), ("r", r), ("i", i), ("z", z), ("y", y)):
-        if t is None and name == "z":
-            at.append((0, 0))
-            continue
-        if t.dtype != x.dtype or t.shape != x.shape or t.device != dev:
-            raise ValueError(f"{name}: expected {tuple(x.shape)} {x.dtype} on {dev}")
-        rs, cs = t.stride()
-        if cs != 1 and d > 1:
-            raise ValueError(f"{name}: channels must be next to each other (stride {cs})")
-        at.append((t.data_ptr(), rs))
+    io, dtype, shape, dev = _io(x, 2)
+    b, d = shape
+    like = (x, dtype, shape, dev)
+    at = (x.data_ptr(), _like(r, "r", *like), _like(i, "i", *like), 0 if z is None else _like(z, "z", *like), _like(y, "y", *like))
+    strides = (x.stride(), r.stride(), i.stride(), (0, 1) if z is None else z.stride(), y.stride())
+    (xs, xc), (rs, rc), (is_, ic), (zs, zc), (ys, yc) = strides
+    if state.dtype is not torch.float32 or state.dim() != 2 or state.shape[1] != d or state.get_device() != dev:
+        raise ValueError(f"state: expected (slots, {d}) torch.float32 on cuda:{dev}")
+    ss, sc = state.stride()
+    if not xc == rc == ic == zc == yc == sc == 1 and d > 1:
+        raise ValueError("channels must be next to each other (stride 1) in x, r, i, z, y and state")
     if lam is None:
         raise ValueError("lam is required")
-    if state.dtype != torch.float32 or state.dim() != 2 or state.shape[1] != d or state.device != dev:
-        raise ValueError(f"state: expected (slots, {d}) torch.float32 on {dev}")
-    ss, cs = state.stride()
-    if cs != 1 and d > 1:
-        raise ValueError(f"state: channels must be next to each other (stride {cs})")
-    (xp, xs), (rp, rs), (ip, is_), (zp, zs), (yp, ys) = at
     ch = (d,)
-    args = _STEP.pack(state.data_ptr(), ss, _dense(slots, "slots", (b,), _I32, dev), xp, rp, ip, zp, yp, xs, rs, is_, zs, ys,
+    args = _STEP.pack(state.data_ptr(), ss, _dense(slots, "slots", (b,), _I32, dev), *at, xs, rs, is_, zs, ys,
                       _dense(lam, "lam", ch, _F32, dev), _dense(r_bias, "r_bias", ch, _F32, dev),
                       _dense(i_bias, "i_bias", ch, _F32, dev), b, d, state.shape[0], io, c)
-    code = _call(x, stream, binding.load().ssm_gated_state_update, args)
+    code = _call(dev, stream, _lib().ssm_gated_state_update, args)
     if check:
         _check(code, "ssm_gated_state_update")
     return code
