@@ -11,7 +11,6 @@
  *   h_t    = a_t h_{t-1} + m_t iota_t x[b,d,t]
  *   y_t    = h_t * silu(z[b,d,t])                 (y_t = h_t without z)
  *   h_{-1} = 0 (or a given initial state);  last_state = h_{length-1}
- * (A gate below 2^-63, about 1e-19, may count as anything up to 2^-63.)
  *
  * Conventions: those of ssm_scan.h (device pointers owned by the caller, no device memory
  * allocated, calls asynchronous on `stream`, status codes), and:

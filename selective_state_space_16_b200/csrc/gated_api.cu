@@ -123,6 +123,14 @@ ssm_status_t ssm_gated_scan_fwd(const ssm_gated_args_t* args, ssm_gated_out_t y,
     if (!rows) return SSM_OK;
     st = check_device(nullptr);
     if (st != SSM_OK) return st;
+    if (p.L == 0) {  // no steps (and, with torch, no addresses): the state passes through
+        const size_t bytes = static_cast<size_t>(p.batch) * p.dim * sizeof(float);
+        cudaError_t e = cudaSuccess;
+        if (last_state && p.h0 != last_state)
+            e = p.h0 ? cudaMemcpyAsync(last_state, p.h0, bytes, cudaMemcpyDeviceToDevice, reinterpret_cast<cudaStream_t>(stream))
+                     : cudaMemsetAsync(last_state, 0, bytes, reinterpret_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? SSM_OK : SSM_ERR_LAUNCH;
+    }
     p.last = last_state;
     p.ckpt = static_cast<float*>(checkpoints);
     return launch_fwd(args->io_dtype, p, reinterpret_cast<cudaStream_t>(stream));

@@ -7,6 +7,7 @@
 #include <cmath>
 
 #include "common.cuh"
+#include "gated_poly.cuh"
 #include "scan_math.cuh"
 
 namespace ssm {
@@ -95,64 +96,80 @@ __device__ __forceinline__ float softplus_lam(float lam) {
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// min that keeps a NaN.
-__device__ __forceinline__ float min_nan(float x, float limit) {
-    float y;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(limit));
-    return y;
+// 1 + y P(y) for the polynomials of gated_poly.cuh, for two steps.
+template <int DEG>
+__device__ __forceinline__ float2 poly2(float2 y, const float (&c)[DEG]) {
+    float2 p = both(c[DEG - 1]);
+#pragma unroll
+    for (int k = DEG - 2; k >= 0; --k) p = __ffma2_rn(y, p, both(c[k]));
+    return __ffma2_rn(y, p, both(1.f));
 }
 
-// Both gates of two steps: rho = sigmoid(r + r_bias), iota = sigmoid(i + i_bias) from kr = -log2(e)
-// r_bias and ki likewise, and Er = e^{-(r + r_bias)}, Ei (1 - rho = Er rho without cancellation).
-// One reciprocal serves a step's two gates, 1 / ((1 + Er)(1 + Ei)), as the special-function unit is
-// the scarcest.  So that the product stays finite a gate below 2^-63 counts as 2^-63.
-struct Gates {
-    float2 rho, iota, Er, Ei;
+// The coefficients of two steps from their gates' pre-activations.  With E = e^{-(r + r_bias)} (kr is
+// -log2(e) r_bias) and root = sqrt(2 c softplus(lam)): Q = root / sqrt(1 + E), so that Q^2 = 2 v.
+// A shut gate, E = inf, gives Q = 0 and with it exactly a = 1 and m = 0.
+//   a = e^{-v}, m = sqrt(1 - a^2), and v / m for the backward
+// are polynomials in 2 v up to v = 1/8, where 1 - a^2 would cancel; beyond it the cancellation costs at
+// most 2e-6 of it and they are formed as written.  NEAR: c softplus(lam) <= 1/8, so that no step of
+// the channel is beyond it (channels with a memory of some ten steps or more), which saves an
+// exponential and a root.  For both element types in fp32: so are the state and the parameters'
+// gradients.
+constexpr float kNear = 0.5f;  // root of a channel at the border, sqrt(2 / 8)
+
+struct Decay {
+    float2 a, m;
+    float2 E, rho, v, v_over_m;  // (backward)
 };
 
-__device__ __forceinline__ Gates gates_of(float2 r, float2 i, float kr, float ki) {
-    const float2 yr = __ffma2_rn(both(-kLog2e), r, both(kr)), yi = __ffma2_rn(both(-kLog2e), i, both(ki));
-    Gates g;
-    g.Er = make_float2(ex2_mufu(min_nan(yr.x, 63.f)), ex2_mufu(min_nan(yr.y, 63.f)));
-    g.Ei = make_float2(ex2_mufu(min_nan(yi.x, 63.f)), ex2_mufu(min_nan(yi.y, 63.f)));
-    const float2 dr = __fadd2_rn(both(1.f), g.Er), di = __fadd2_rn(both(1.f), g.Ei), d = __fmul2_rn(dr, di);
-    const float2 inv = make_float2(rcp_approx(d.x), rcp_approx(d.y));
-    g.rho = __fmul2_rn(inv, di);
-    g.iota = __fmul2_rn(inv, dr);
+template <bool NEAR, bool BACKWARD>
+__device__ __forceinline__ Decay decay_of(float2 r, float kr, float2 root) {
+    constexpr float ca[] = SSM_GATED_DECAY_POLY, cg[] = SSM_GATED_WEIGHT_POLY, ci[] = SSM_GATED_WEIGHT_INV_POLY;
+    Decay d;
+    const float2 x = __ffma2_rn(both(-kLog2e), r, both(kr));
+    d.E = make_float2(ex2_mufu(x.x), ex2_mufu(x.y));
+    const float2 p = __fadd2_rn(both(1.f), d.E);
+    const float2 R = make_float2(rsqrt_approx(p.x), rsqrt_approx(p.y)), Q = __fmul2_rn(root, R), y = __fmul2_rn(Q, Q);
+    d.a = poly2(y, ca);
+    d.m = __fmul2_rn(Q, poly2(y, cg));
+    if constexpr (BACKWARD) {
+        const float2 h = __fmul2_rn(both(0.5f), Q);
+        d.rho = __fmul2_rn(R, R);
+        d.v = __fmul2_rn(h, Q);
+        d.v_over_m = __fmul2_rn(h, poly2(y, ci));
+    }
+    if constexpr (!NEAR) {
+        const float2 half = __fmul2_rn(both(-0.5f * kLog2e), y);
+        const float2 e = make_float2(ex2_mufu(half.x), ex2_mufu(half.y));
+        const bool nx = y.x < 0.25f, ny = y.y < 0.25f;
+        d.a = make_float2(nx ? d.a.x : e.x, ny ? d.a.y : e.y);
+        const float2 m2 = __ffma2_rn(make_float2(-e.x, -e.y), e, both(1.f));
+        if constexpr (BACKWARD) {
+            const float2 rs = make_float2(rsqrt_approx(m2.x), rsqrt_approx(m2.y));
+            d.m = make_float2(nx ? d.m.x : m2.x * rs.x, ny ? d.m.y : m2.y * rs.y);
+            d.v_over_m = make_float2(nx ? d.v_over_m.x : d.v.x * rs.x, ny ? d.v_over_m.y : d.v.y * rs.y);
+        } else {
+            d.m = make_float2(nx ? d.m.x : sqrt_approx(m2.x), ny ? d.m.y : sqrt_approx(m2.y));
+        }
+    }
+    return d;
+}
+
+// e^{-(i + i_bias)} and sigmoid(i + i_bias) of two steps (ki = -log2(e) i_bias).
+struct Gate {
+    float2 E, sig;
+};
+
+__device__ __forceinline__ Gate gate_of(float2 i, float ki) {
+    const float2 x = __ffma2_rn(both(-kLog2e), i, both(ki));
+    Gate g;
+    g.E = make_float2(ex2_mufu(x.x), ex2_mufu(x.y));
+    const float2 d = __fadd2_rn(both(1.f), g.E);
+    g.sig = make_float2(rcp_approx(d.x), rcp_approx(d.y));
     return g;
 }
 
-// The decay a = e^x and 1 - a^2 = -w (2 + w), w = a - 1, of two steps with x = -v <= 0.  Near a = 1 the
-// difference w cancels, so for v < 1/8 the series w = x (1 + x/2 + x^2/6 + x^3/24 + x^4/120) takes its
-// place (the first term left out is 4e-8 of the sum there; beyond it the cancellation costs at most
-// 2e-6 of w), and a = 1 + w is then good to half a step.  For both element types: the state and the
-// parameters' gradients are fp32.  NEAR: c softplus(lam) < 1/8, so that no step of the channel needs
-// the exponential: channels with a memory of some ten steps or more.
-constexpr float kNear = 0.125f;
-
-struct Decay {
-    float2 a, m2;  // m2 = 1 - a^2
-};
-
-template <bool NEAR>
-__device__ __forceinline__ Decay decay_of(float2 x) {
-    float2 p = __ffma2_rn(x, both(1.f / 120), both(1.f / 24));
-    p = __ffma2_rn(x, p, both(1.f / 6));
-    p = __ffma2_rn(x, p, both(0.5f));
-    float2 w = __ffma2_rn(__fmul2_rn(x, x), p, x);
-    Decay d;
-    if constexpr (NEAR) {
-        d.a = __fadd2_rn(both(1.f), w);
-    } else {
-        const float2 y = __fmul2_rn(x, both(kLog2e));
-        const float2 e = make_float2(ex2_mufu(y.x), ex2_mufu(y.y)), f = __fadd2_rn(e, both(-1.f));
-        w = make_float2(x.x > -kNear ? w.x : f.x, x.y > -kNear ? w.y : f.y);
-        const float2 near = __fadd2_rn(both(1.f), w);
-        d.a = make_float2(x.x > -kNear ? near.x : e.x, x.y > -kNear ? near.y : e.y);
-    }
-    d.m2 = __fmul2_rn(w, __ffma2_rn(both(-1.f), w, both(-2.f)));
-    return d;
-}
+// 1 - s of a sigmoid s = 1 / (1 + E) without cancellation.
+__device__ __forceinline__ float2 rest_of(float2 E, float2 s) { return __fmul2_rn(make_float2(fminf(E.x, 1e38f), fminf(E.y, 1e38f)), s); }
 
 __device__ __forceinline__ float2 sigmoid2(float2 z) {
     const float2 y = __fmul2_rn(both(-kLog2e), z);
@@ -239,11 +256,24 @@ __device__ __forceinline__ void load_elements(const IO* row, int t0, int len, Ra
     for (int k = 0; k < kWords / 4; ++k) g.v[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
 }
 
+// Which steps of a row may be read as whole vectors: up to 15 before and behind it, as far as that is
+// inside every operand (a row's neighbours are).  So only the ends of an operand are read by elements.
+struct Reach {
+    int low, high;
+};
+
+__device__ __forceinline__ void narrow(Reach& reach, const GatedTensor& t, int b, int d, int batch, int dim) {
+    const long long at = b * t.bs + d * t.ds, most = (batch - 1) * t.bs + (dim - 1) * t.ds;
+    const bool up = t.bs >= 0 && t.ds >= 0;
+    reach.low = max(reach.low, up ? -static_cast<int>(min(at, 15LL)) : 0);
+    reach.high = min(reach.high, up ? static_cast<int>(min(most - at, 15LL)) : 0);
+}
+
 // Steps [t0, t0 + N) of the operands, those of them inside [0, len); the others are anything.
 template <typename IO, int N, int IN>
-__device__ __forceinline__ void load_steps(const IO* const (&in)[IN], const bool (&vec)[IN], bool all_vec, int t0, int len, int L,
+__device__ __forceinline__ void load_steps(const IO* const (&in)[IN], const bool (&vec)[IN], bool all_vec, int t0, int len, Reach reach,
                                            Raw<IO, N> (&g)[IN]) {
-    const bool whole = t0 >= 0 && t0 + N <= L;
+    const bool whole = t0 >= reach.low && t0 + N <= reach.high;
     if (all_vec && whole && t0 < len) {
 #pragma unroll
         for (int k = 0; k < IN; ++k) load_vectors(in[k], t0, g[k]);
@@ -273,9 +303,10 @@ struct Ring {
         for (int j = 0; j < kV; ++j) cp_async_16(slot(ring, stage, k * kV + j), q + j, 16);
     }
     // One group of copies.
-    __device__ static void load(uint4* ring, int stage, const IO* const (&in)[IN], const bool (&vec)[IN], bool all_vec, int t0, int len, int L) {
-        const bool whole = t0 >= 0 && t0 + N <= L;
-        if (all_vec && whole && t0 < len) {
+    __device__ static void load(uint4* ring, int stage, const IO* const (&in)[IN], const bool (&vec)[IN], bool all_vec, int t0, int len,
+                                Reach reach) {
+        const bool whole = t0 >= reach.low && t0 + N <= reach.high;
+        if (all_vec && whole && t0 < len && t0 + N > 0) {
 #pragma unroll
             for (int k = 0; k < IN; ++k) copy(ring, stage, k, in[k], t0);
         } else if (t0 < len && t0 + N > 0) {

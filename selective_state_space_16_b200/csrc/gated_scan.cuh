@@ -107,11 +107,15 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     bool vec[kIn], all_vec = true;
 #pragma unroll
     for (int k = 0; k < kIn; ++k) all_vec &= vec[k] = phase_of(in[k]) == phase;
+    Reach reach{-15, 15};
+    for (const GatedTensor* q : {&p.x, &p.r, &p.i}) narrow(reach, *q, b, d, p.batch, p.dim);
+    if (GATE) narrow(reach, p.z, b, d, p.batch, p.dim);
+    reach.high += p.L;
     const bool vy = phase_of(y) == phase, vz[1] = {phase_of(zrow[0]) == phase};
     const unsigned char* reset = RESET ? p.reset + static_cast<long long>(b) * p.L : nullptr;
     const unsigned char* reset_end = RESET ? p.reset + static_cast<long long>(p.batch) * p.L : nullptr;
-    const float rate = -p.c * softplus_lam(p.lam[d]);
-    const bool near = rate > -kNear;
+    const float root = sqrtf(2.f * p.c * softplus_lam(p.lam[d]));
+    const bool near = root <= kNear;
     const float rb = -kLog2e * (p.r_bias ? p.r_bias[d] : 0.f), ib = -kLog2e * (p.i_bias ? p.i_bias[d] : 0.f);
     float carry = p.h0 && valid ? p.h0[row] : 0.f;
     float* ckpt = p.ckpt ? p.ckpt + sizeof(CkptHeader) / 4 + row * p.ckpt_row : nullptr;
@@ -125,28 +129,26 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     int t0 = (at.part * SEG + at.lane) * N - phase;
     const int stride = at.parts * SEG * N;
     Raw<IO, N> next[kIn];
-    if (kAhead) load_steps(in, vec, all_vec, t0, valid ? p.L : 0, p.L, next);  // (not waiting for len)
+    if (kAhead) load_steps(in, vec, all_vec, t0, valid ? p.L : 0, reach, next);  // (not waiting for len)
     int round = 0;
 #pragma unroll 1
     for (int t = -phase; SEG == 32 ? t < len : __any_sync(kAll, t < len); t += stride, t0 += stride, ++round) {
         float2 a[kPairs], u[kPairs], v[kPairs], w[kPairs];
-        if (!kAhead) load_steps(in, vec, all_vec, t0, len, p.L, next);
+        if (!kAhead) load_steps(in, vec, all_vec, t0, len, reach, next);
         unpack<IO, N>(next[0], u);
         unpack<IO, N>(next[1], v);
         unpack<IO, N>(next[2], w);
         Raw<IO, N> zc[1];
-        if (GATE) load_steps(zrow, vz, vz[0], t0, len, p.L, zc);  // wanted last
-        if (kAhead) load_steps(in, vec, all_vec, t0 + stride, len, p.L, next);  // under way while this tile is computed
+        if (GATE) load_steps(zrow, vz, vz[0], t0, len, reach, zc);  // wanted last
+        if (kAhead) load_steps(in, vec, all_vec, t0 + stride, len, reach, next);  // under way while this tile is computed
         const auto coefficients = [&](auto near_tag) {
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) {
-                const Gates gt = gates_of(v[k], w[k], rb, ib);
-                const Decay dec = decay_of<decltype(near_tag)::value>(__fmul2_rn(both(rate), gt.rho));
+                const Decay dec = decay_of<decltype(near_tag)::value, false>(v[k], rb, both(root));
                 a[k] = dec.a;
-                const float2 m = make_float2(sqrt_approx(dec.m2.x), sqrt_approx(dec.m2.y));
-                u[k] = __fmul2_rn(u[k], gt.iota);
+                u[k] = __fmul2_rn(u[k], gate_of(w[k], ib).sig);
                 if (RESET) v[k] = u[k];  // (m_t = 1 at a reset)
-                u[k] = __fmul2_rn(u[k], m);
+                u[k] = __fmul2_rn(u[k], dec.m);
             }
         };
         if (near)
@@ -243,11 +245,15 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     for (int k = 0; k < kIn; ++k) all_vec &= vin[k] = phase_of(in[k]) == phase;
 #pragma unroll
     for (int k = 0; k < kOut; ++k) all_vec &= vout[k] = phase_of(out[k]) == phase;
+    Reach reach{-15, 15};
+    for (const GatedTensor* q : {&p.x, &p.r, &p.i, &p.dy}) narrow(reach, *q, b, d, p.batch, p.dim);
+    if (GATE) narrow(reach, p.z, b, d, p.batch, p.dim);
+    reach.high += p.L;
     const unsigned char* reset = RESET ? p.reset + static_cast<long long>(b) * p.L : nullptr;
     const unsigned char* reset_end = RESET ? p.reset + static_cast<long long>(p.batch) * p.L : nullptr;
     const float* ckpt = p.ckpt + sizeof(CkptHeader) / 4 + row * p.ckpt_row;
-    const float rate = -p.c * softplus_lam(p.lam[d]);
-    const bool near = rate > -kNear;
+    const float root = sqrtf(2.f * p.c * softplus_lam(p.lam[d]));
+    const bool near = root <= kNear;
     const float rb = -kLog2e * (p.r_bias ? p.r_bias[d] : 0.f), ib = -kLog2e * (p.i_bias ? p.i_bias[d] : 0.f);
     float carry = p.dlast && valid ? p.dlast[row] : 0.f;  // a_{t+1} g_{t+1}: what the steps after the tile send back
     float2 sumT = both(0.f), sumr = both(0.f), sumi = both(0.f);
@@ -267,7 +273,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         const int t0 = t + (at.part * SEG + at.lane) * N;
         const bool active = t >= -phase;
         if (active && t0 < len) cp_async_4(states_in + stage * blockDim.x, ckpt + (t0 + phase) / kGroup);
-        In::load(ring, stage, in, vin, all_vec, t0, active ? len : -N, p.L);
+        In::load(ring, stage, in, vin, all_vec, t0, active ? len : -N, reach);
     };
     int round = 0, stage = 0;
 #pragma unroll
@@ -291,7 +297,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
             stage = stage == kStages - 1 ? 0 : stage + 1;
         } else {
             if (t0 < end && active) h = ckpt[(t0 + phase) / kGroup];
-            load_steps(in, vin, all_vec, t0, active ? end : -N, p.L, raw);
+            load_steps(in, vin, all_vec, t0, active ? end : -N, reach, raw);
         }
         unpack<IO, N>(raw[0], kx);
         unpack<IO, N>(raw[1], kr);
@@ -305,28 +311,25 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         }
         // what g_t is to be multiplied by, for each gradient:
         //   dx  kx = m iota         di  ki = b (1 - iota), b = m iota x
-        //   T = a (iota x a v / m - h_{t-1} v) = h_{t-1} ax - kT       dr  T kr, kr = 1 - rho
+        //   T = a (iota x a v / m - h_{t-1} v) = kT - h_{t-1} ax       dr  T kr, kr = 1 - rho
         const auto coefficients = [&](auto near_tag) {
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) {
-                const Gates gt = gates_of(kr[k], ki[k], rb, ib);
-                const float2 xv = __fmul2_rn(both(rate), gt.rho);  // -v
-                const Decay dec = decay_of<decltype(near_tag)::value>(xv);
-                // v -> 0: m and v / m go to 0
-                const float2 rs = make_float2(rsqrt_approx(fmaxf(dec.m2.x, 1e-30f)), rsqrt_approx(fmaxf(dec.m2.y, 1e-30f)));
-                const float2 ux = __fmul2_rn(gt.iota, kx[k]);
-                float2 m = __fmul2_rn(dec.m2, rs);
+                const Decay dec = decay_of<decltype(near_tag)::value, true>(kr[k], rb, both(root));
+                const Gate gate = gate_of(ki[k], ib);
+                const float2 ux = __fmul2_rn(gate.sig, kx[k]), qa = __fmul2_rn(dec.a, dec.v_over_m);
+                float2 m = dec.m;
                 a[k] = dec.a;
-                ax[k] = __fmul2_rn(dec.a, xv);
-                kT[k] = __fmul2_rn(__fmul2_rn(ax[k], dec.a), __fmul2_rn(rs, ux));
-                kr[k] = __fmul2_rn(gt.Er, gt.rho);
+                ax[k] = __fmul2_rn(dec.a, dec.v);
+                kT[k] = __fmul2_rn(__fmul2_rn(dec.a, qa), ux);
+                kr[k] = rest_of(dec.E, dec.rho);
                 if (RESET && any_cut) {
                     if (flag_of(flags, 2 * k)) a[k].x = kCut, m.x = 1.f, ax[k].x = kT[k].x = 0.f;
                     if (flag_of(flags, 2 * k + 1)) a[k].y = kCut, m.y = 1.f, ax[k].y = kT[k].y = 0.f;
                 }
-                kx[k] = __fmul2_rn(m, gt.iota);
+                kx[k] = __fmul2_rn(m, gate.sig);
                 b[k] = __fmul2_rn(m, ux);
-                ki[k] = __fmul2_rn(b[k], __fmul2_rn(gt.Ei, gt.iota));
+                ki[k] = __fmul2_rn(b[k], rest_of(gate.E, gate.sig));
             }
         };
         if (near)
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
             constexpr bool CUT = decltype(cut_tag)::value;
 #pragma unroll
             for (int e = 0; e < N; ++e) {  // kT becomes T, b the states
-                const float term = fmaf(h, step_of(ax, e), -step_of(kT, e));
+                const float term = fmaf(-h, step_of(ax, e), step_of(kT, e));
                 step_of(kT, e) = CUT && is_cut(step_of(a, e)) ? 0.f : term;
                 step_of(b, e) = h = carry_on<CUT>(step_of(a, e), h, step_of(b, e));
             }

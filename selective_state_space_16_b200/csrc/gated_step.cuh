@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kStepThreads) gated_step_kernel(const GatedSte
     if (slot < 0 || slot >= p.n_slots) return;
     const bool vec = g.vec != 0;
     float* state = p.state + slot * p.state_stride;
-    float h[kStepChannels], x[kStepChannels], r[kStepChannels], i[kStepChannels], z[kStepChannels], rate[kStepChannels],
+    float h[kStepChannels], x[kStepChannels], r[kStepChannels], i[kStepChannels], z[kStepChannels], root[kStepChannels],
         rb[kStepChannels] = {}, ib[kStepChannels] = {};
     const auto load_row = [&](int k) {
         load4(static_cast<const IO*>(p.x) + k * p.x_stride, d, p.dim, vec, x);
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kStepThreads) gated_step_kernel(const GatedSte
     };
     load4(state, d, p.dim, vec, h);
     load_row(b);
-    load4(p.lam, d, p.dim, vec, rate);
+    load4(p.lam, d, p.dim, vec, root);
     if (p.r_bias) load4(p.r_bias, d, p.dim, vec, rb);
     if (p.i_bias) load4(p.i_bias, d, p.dim, vec, ib);
     bool again = false;
@@ -83,20 +83,19 @@ __global__ void __launch_bounds__(kStepThreads) gated_step_kernel(const GatedSte
     }
     if (d >= p.dim) return;
 #pragma unroll
-    for (int k = 0; k < kStepChannels; ++k) rate[k] = -p.c * softplus_lam(rate[k]);
+    for (int k = 0; k < kStepChannels; ++k) root[k] = sqrtf(2.f * p.c * softplus_lam(root[k]));
     for (int row = b;;) {
 #pragma unroll
         for (int k = 0; k < kStepChannels; k += 2) {
             const float2 hv = make_float2(h[k], h[k + 1]), xv = make_float2(x[k], x[k + 1]);
-            const Gates gt = gates_of(make_float2(r[k] + rb[k], r[k + 1] + rb[k + 1]), make_float2(i[k] + ib[k], i[k + 1] + ib[k + 1]), 0.f, 0.f);
-            const Decay dec = decay_of<false>(__fmul2_rn(make_float2(rate[k], rate[k + 1]), gt.rho));
-            const float2 m = make_float2(sqrt_approx(dec.m2.x), sqrt_approx(dec.m2.y));
-            const float2 now = __ffma2_rn(dec.a, hv, __fmul2_rn(__fmul2_rn(m, gt.iota), xv));
+            const Decay dec = decay_of<false, false>(make_float2(r[k] + rb[k], r[k + 1] + rb[k + 1]), 0.f, make_float2(root[k], root[k + 1]));
+            const Gate gate = gate_of(make_float2(i[k] + ib[k], i[k + 1] + ib[k + 1]), 0.f);
+            const float2 now = __ffma2_rn(dec.a, hv, __fmul2_rn(__fmul2_rn(dec.m, gate.sig), xv));
             h[k] = now.x, h[k + 1] = now.y;
             float2 out = now;
             if (GATE) {
                 const float2 zv = make_float2(z[k], z[k + 1]);
-                out = __fmul2_rn(now, __fmul2_rn(zv, sigmoid2(zv)));
+                out = __fmul2_rn(now, gate_silu2<IO>(zv));
             }
             x[k] = out.x, x[k + 1] = out.y;
         }

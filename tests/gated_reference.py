@@ -3,17 +3,14 @@ what the same computation in 32 bits can be off.
 
 The bound follows the kernels' arithmetic with u = 2^-23 (one step of fp32 relative to the value;
 a rounding is half of it):
-  a = 2^(rate rho): rho's argument is rounded (|r| u of e^-r), its exponential, sum and reciprocal
-  cost 4 u, the rate 4 u, their product enters a multiplied by v; the exponential itself costs 2 u:
-      e_a = (3 + v (|r| + 8)) u   relative;
-  b = m iota x: m is the root of 1 - a^2, whose series or difference is off by 24 u at the border
-  between the two (half of it in m); iota as rho:   e_b = (22 + |r| + |i|) u   relative;
+  v = root^2 / (2 (1 + E)): E = e^-r from a rounded argument, (|r| + 2) u; the sum 0.5 u; its reciprocal root
+  1.1 u and root = sqrt(2 c softplus(lam)) 2.5 u, a product 0.5 u, all three doubled by the square, 0.5 u; in all
+  (|r| + 11) u of v, and so v times that of a = e^-v, whose exponential or polynomial costs 2 u more:
+      e_a = (3 + v (|r| + 11)) u   relative;
+  b = m iota x: m is a polynomial in v times sqrt(v), or the root of 1 - a^2, which is off by 24 u at the border
+  between the two (half of it in m); iota = 1 / (1 + e^-i) 4 u + |i| u:   e_b = (22 + |r| + |i|) u   relative;
   the state's error E_t = a_t (E_{t-1} + (e_a + u) H_{t-1}) + (e_b + u) |b_t|  with H the recurrence of |b|.
 Composing stretches in another order has as many roundings on every path again: E doubled.
-A gate below 2^-63 may count as anything up to 2^-63 (ssm_gated.h).  An input gate is then off by at most
-2^-63, which adds m |x| 2^-63 to the error of b and so on; a recurrence gate moves v by at most
-dv = c softplus(lam) 2^-63, so that a moves by at most dv, and m = sqrt(1 - e^{-2v}) and v / m <= sqrt(v),
-both between their values at 0 and at dv, by at most sqrt(2 dv) and sqrt(dv).
 y of bf16 is gated by z (1 + tanh(z / 2)) / 2 with tanh.approx, at most 2^-10.98 off relative to tanh and so at most
 2^-11.9 |z| off in silu(z); the other gates are as above.
 bf16 results are rounded once more, by at most 2^-8 of their value; inputs of bf16 enter as they are.
@@ -47,13 +44,9 @@ def reference(x, r, i, lam, r_bias=None, i_bias=None, z=None, initial_state=None
         v = c * soft[:, None] * rho
         a, m = np.exp(-v), np.sqrt(-np.expm1(-2 * v))
         a, m = np.where(cut[:, None], 0, a), np.where(cut[:, None], 1, m)
-        ea = (3 + v * (np.abs(r) + 8)) * U
+        ea = (3 + v * (np.abs(r) + 11)) * U
         eb = (22 + np.abs(r) + np.abs(i)) * U
         b = m * iota * x
-        floor = 2.0 ** -63
-        di_ = np.where(iota < 2 * floor, floor, 0)  # what the floor can move a gate by
-        dv_ = np.where(rho < 2 * floor, c * soft[:, None] * floor, 0)
-        babs = np.where(np.isfinite(x), (m * di_ + np.sqrt(2 * dv_) * (iota + di_)) * np.abs(x), 0)
         h = np.zeros((B, D)) if h0 is None else h0.copy()
         H, E = np.abs(h), np.abs(h) * U
         hs, Es, before, Ebefore = (np.zeros((B, D, L)) for _ in range(4))
@@ -62,7 +55,7 @@ def reference(x, r, i, lam, r_bias=None, i_bias=None, z=None, initial_state=None
             before[..., t], Ebefore[..., t] = h, E
             keep = cut[:, t][:, None]  # nothing reaches over a reset, not even a NaN
             new = np.where(keep, 0, a[..., t] * h) + b[..., t]
-            E = np.where(on, np.where(keep, 0, a[..., t] * (E + (ea[..., t] + U) * H)) + (eb[..., t] + U) * np.abs(b[..., t]) + babs[..., t] + dv_[..., t] * H, E)
+            E = np.where(on, np.where(keep, 0, a[..., t] * (E + (ea[..., t] + U) * H)) + (eb[..., t] + U) * np.abs(b[..., t]), E)
             H = np.where(on, np.where(keep, 0, a[..., t] * H) + np.abs(b[..., t]), H)
             h = np.where(on, new, h)
             hs[..., t], Es[..., t] = h, E
@@ -99,13 +92,11 @@ def reference(x, r, i, lam, r_bias=None, i_bias=None, z=None, initial_state=None
             e = eb[..., t] + (20 + np.abs(r[..., t]) + np.abs(i[..., t])) * U
             Tk = np.where(keep, 0, at * (k1 - k2))
             eTk = np.where(keep, 0, at * ((np.abs(k1) + np.abs(k2)) * e + 2 * Eb * vt))
-            sx = np.abs(x[..., t])
-            eTk = eTk + np.where(keep, 0, (io + di_[..., t]) * sx * np.sqrt(dv_[..., t]) + di_[..., t] * sx * q + np.abs(hb) * dv_[..., t])
             T[..., t], eT[..., t] = g * Tk, eg * np.abs(Tk) + ga * eTk
             dr[..., t], edr[..., t] = g * Tk * (1 - rh), (eg * np.abs(Tk) + ga * (eTk + np.abs(Tk) * e)) * sigmoid(-r[..., t])
             ki, kx = mt * io * x[..., t] * sigmoid(-i[..., t]), mt * io
-            di[..., t], edi[..., t] = g * ki, (eg + ga * e) * np.abs(ki) + ga * babs[..., t]
-            dx[..., t], edx[..., t] = g * kx, (eg + ga * e) * kx + ga * (mt * di_[..., t] + np.sqrt(2 * dv_[..., t]) * (io + di_[..., t]))
+            di[..., t], edi[..., t] = g * ki, (eg + ga * e) * np.abs(ki)
+            dx[..., t], edx[..., t] = g * kx, (eg + ga * e) * kx
             ns, nSg, nSa = np.where(keep, 0, at * g), np.where(keep, 0, at * (eg + (ea[..., t] + U) * ga)), np.where(keep, 0, at * ga)
             s, Sg, Sa = np.where(on, ns, s), np.where(on, nSg, Sg), np.where(on, nSa, Sa)
         dr = T * sigmoid(-r)

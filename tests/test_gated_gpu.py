@@ -193,6 +193,9 @@ def test_wanted_gradients_only(cuda_device):
 
 def test_empty(cuda_device):
     lam = torch.zeros(4, device="cuda")
+    wide = torch.randn(2, 4, 13, device="cuda")[..., 5:5]  # (an empty slice has no address, but its strides)
+    y, last = ssm.gated_scan_fwd(wide, wide, wide, lam, z=wide)
+    assert y.shape == (2, 4, 0) and not bool(last.any())
     for B, L in ((2, 0), (0, 5)):
         x = torch.empty(B, 4, L, device="cuda", dtype=torch.bfloat16)
         h0 = torch.randn(B, 4, device="cuda")
