@@ -42,8 +42,11 @@ long long checkpoint_row(int64_t seqlen) {
     return static_cast<long long>(round_up((static_cast<size_t>(seqlen) + 2 * (ssm::kGroup - 1)) / ssm::kGroup, 4));
 }
 
-GatedTensor tensor(const ssm_gated_in_t& t) { return {t.data, t.batch_stride, t.dim_stride}; }
-GatedTensor tensor(const ssm_gated_out_t& t) { return {t.data, t.batch_stride, t.dim_stride}; }
+template <typename T>
+GatedTensor tensor(const T& t, int batch, int dim) {
+    const bool up = t.batch_stride >= 0 && t.dim_stride >= 0;
+    return {t.data, t.batch_stride, t.dim_stride, (batch - 1LL) * t.batch_stride + (dim - 1LL) * t.dim_stride, up ? 15 : 0};
+}
 
 bool element_aligned(const void* p, int io) {
     return (reinterpret_cast<uintptr_t>(p) & (io == SSM_BF16 ? 1u : 3u)) == 0;
@@ -65,10 +68,10 @@ ssm_status_t common_params(const ssm_gated_args_t* a, GatedParams* p) {
                           static_cast<const void*>(a->initial_state), static_cast<const void*>(a->lengths)})
         if (!float_aligned(q)) return SSM_ERR_INVALID_ARG;
     *p = GatedParams{};
-    p->x = tensor(a->x);
-    p->r = tensor(a->r);
-    p->i = tensor(a->i);
-    p->z = tensor(a->z);
+    p->x = tensor(a->x, a->batch, a->dim);
+    p->r = tensor(a->r, a->batch, a->dim);
+    p->i = tensor(a->i, a->batch, a->dim);
+    p->z = tensor(a->z, a->batch, a->dim);
     p->lam = a->lam;
     p->r_bias = a->r_bias;
     p->i_bias = a->i_bias;
@@ -118,7 +121,7 @@ ssm_status_t ssm_gated_scan_fwd(const ssm_gated_args_t* args, ssm_gated_out_t y,
     if (rows && p.L > 0 && !y.data) return SSM_ERR_INVALID_ARG;
     if (is_input(args, y.data) || !element_aligned(y.data, args->io_dtype)) return SSM_ERR_INVALID_ARG;
     if (!float_aligned(last_state) || !aligned16(checkpoints)) return SSM_ERR_INVALID_ARG;
-    p.y = tensor(y);
+    p.y = tensor(y, p.batch, p.dim);
     if (rows && p.L > 0 && !rows_apart(p.y, p.batch, p.dim, p.L)) return SSM_ERR_INVALID_ARG;
     if (!rows) return SSM_OK;
     st = check_device(nullptr);
@@ -158,11 +161,11 @@ ssm_status_t ssm_gated_scan_bwd(const ssm_gated_args_t* args, const ssm_gated_gr
     for (const void* q : {static_cast<const void*>(g.dlast_state), static_cast<const void*>(g.dlam), static_cast<const void*>(g.dr_bias),
                           static_cast<const void*>(g.di_bias), static_cast<const void*>(g.dinitial_state)})
         if (!float_aligned(q)) return SSM_ERR_INVALID_ARG;
-    p.dy = tensor(g.dy);
-    p.dx = tensor(g.dx);
-    p.dr = tensor(g.dr);
-    p.di = tensor(g.di);
-    p.dz = tensor(g.dz);
+    p.dy = tensor(g.dy, p.batch, p.dim);
+    p.dx = tensor(g.dx, p.batch, p.dim);
+    p.dr = tensor(g.dr, p.batch, p.dim);
+    p.di = tensor(g.di, p.batch, p.dim);
+    p.dz = tensor(g.dz, p.batch, p.dim);
     if (rows && p.L > 0)
         for (const GatedTensor* t : {&p.dx, &p.dr, &p.di, p.z.p ? &p.dz : &p.dx})
             if (!rows_apart(*t, p.batch, p.dim, p.L)) return SSM_ERR_INVALID_ARG;

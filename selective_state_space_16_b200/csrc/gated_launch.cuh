@@ -8,26 +8,28 @@
 
 namespace ssmh {
 
-// How rows are laid on lanes.  Short rows share a warp (2 or 8 lanes of 8 steps each); few long rows are
-// split over the warps of a block until the GPU has work for all its SMs.
+// How rows are laid on lanes, each of which holds `steps` steps.  Rows that fit in half a warp share one;
+// few long rows are split over the warps of a block until the GPU has work for all its SMs.
 struct GatedShape {
     int seg, split;
 };
 
-inline GatedShape gated_shape(long long rows, int L) {
-    if (L <= 2 * ssm::kGroup) return {2, 1};
-    if (L <= 8 * ssm::kGroup) return {8, 1};
-    int split = 1;
-    while (split < ssm::kMaxSplit && rows * split < 148 * 16 && split * 32 * ssm::kGroup < L) split *= 2;
-    return {32, split};
+template <typename IO>
+GatedShape gated_shape(long long rows, int L, int steps) {
+    constexpr int kVec = 16 / sizeof(IO);
+    const long long need = L % kVec ? L + static_cast<long long>(kVec) - 1 : L;  // (rows then start anywhere in a vector)
+    int seg = 1, split = 1;
+    while (seg < 32 && static_cast<long long>(seg) * steps < need) seg *= 2;
+    if (seg == 32)
+        while (split < ssm::kMaxSplit && rows * split < 148 * 10 && static_cast<long long>(split) * 32 * steps < L) split *= 2;
+    return {seg, split};
 }
 
 using GatedKernel = void (*)(const ssm::GatedParams);
 
 template <typename IO, bool GATE, bool RESET>
 GatedKernel gated_kernel(GatedShape shape, bool backward) {
-    if (shape.seg == 2) return backward ? ssm::gated_bwd_kernel<IO, GATE, RESET, 2, false> : ssm::gated_fwd_kernel<IO, GATE, RESET, 2, false>;
-    if (shape.seg == 8) return backward ? ssm::gated_bwd_kernel<IO, GATE, RESET, 8, false> : ssm::gated_fwd_kernel<IO, GATE, RESET, 8, false>;
+    if (shape.seg < 32) return backward ? ssm::gated_bwd_kernel<IO, GATE, RESET, 0, false> : ssm::gated_fwd_kernel<IO, GATE, RESET, 0, false>;
     if (shape.split > 1) return backward ? ssm::gated_bwd_kernel<IO, GATE, RESET, 32, true> : ssm::gated_fwd_kernel<IO, GATE, RESET, 32, true>;
     return backward ? ssm::gated_bwd_kernel<IO, GATE, RESET, 32, false> : ssm::gated_fwd_kernel<IO, GATE, RESET, 32, false>;
 }
@@ -35,7 +37,8 @@ GatedKernel gated_kernel(GatedShape shape, bool backward) {
 template <typename IO>
 ssm_status_t launch_gated(ssm::GatedParams p, bool backward, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.batch) * p.dim;
-    const GatedShape shape = gated_shape(rows, p.L);
+    const GatedShape shape = gated_shape<IO>(rows, p.L, backward ? ssm::kBwdSteps : ssm::kFwdSteps<IO>);
+    p.seg = shape.seg;
     p.split = shape.split;
     const bool gate = p.z.p != nullptr, reset = p.reset != nullptr;
     const GatedKernel kern = gate ? (reset ? gated_kernel<IO, true, true>(shape, backward) : gated_kernel<IO, true, false>(shape, backward))

@@ -16,6 +16,8 @@ namespace ssm {
 struct GatedTensor {
     const void* p;
     long long bs, ds;
+    long long most;    // where the last row starts
+    long long before;  // elements beside a row that may be read where the operand has them: 15, or 0 (odd strides)
 };
 
 struct GatedParams {
@@ -28,6 +30,7 @@ struct GatedParams {
     int batch, dim, L;
     long long ckpt_row;
     float c;
+    int seg;    // lanes that share a row
     int split;  // warps that share a row (1: a row per warp or part of one)
     // backward
     GatedTensor dy, dx, dr, di, dz;
@@ -262,11 +265,13 @@ struct Reach {
     int low, high;
 };
 
-__device__ __forceinline__ void narrow(Reach& reach, const GatedTensor& t, int b, int d, int batch, int dim) {
-    const long long at = b * t.bs + d * t.ds, most = (batch - 1) * t.bs + (dim - 1) * t.ds;
-    const bool up = t.bs >= 0 && t.ds >= 0;
-    reach.low = max(reach.low, up ? -static_cast<int>(min(at, 15LL)) : 0);
-    reach.high = min(reach.high, up ? static_cast<int>(min(most - at, 15LL)) : 0);
+// The row (b, d) of an input, which narrows the reach.
+template <typename IO>
+__device__ __forceinline__ const IO* row_in(const GatedTensor& t, int b, int d, Reach& reach) {
+    const long long at = b * t.bs + d * t.ds;
+    reach.low = max(reach.low, -static_cast<int>(min(at, t.before)));
+    reach.high = min(reach.high, static_cast<int>(min(t.most - at, t.before)));
+    return static_cast<const IO*>(t.p) + at;
 }
 
 // Steps [t0, t0 + N) of the operands, those of them inside [0, len); the others are anything.
@@ -366,15 +371,53 @@ __device__ __forceinline__ void store_vectors(IO* row, int t0, float2 (&v)[PAIRS
     }
 }
 
-// The steps that lie in [0, n); `vec`: as vectors where all of them do.
+// Which of the steps [t0, t0 + N) lie in [0, n), a bit each.
+template <int N> constexpr unsigned all_steps = (1u << N) - 1;
+
+template <int N>
+__device__ __forceinline__ unsigned steps_inside(int t0, int n) {
+    unsigned bits = all_steps<N>;
+    if (t0 + N > n) bits = n > t0 ? (1u << (n - t0)) - 1 : 0;  // (n - t0 < N)
+    if (t0 < 0) bits &= t0 > -N ? ~((1u << -t0) - 1) : 0;
+    return bits;
+}
+
+// The steps at the bits; `vec`: as a vector where that is all of them.
 template <typename IO, int PAIRS>
-__device__ __forceinline__ void store_steps(IO* row, int t0, int n, bool vec, float2 (&v)[PAIRS]) {
-    if (vec && t0 >= 0 && t0 + 2 * PAIRS <= n) {
+__device__ __forceinline__ void store_steps(IO* row, int t0, unsigned bits, bool vec, float2 (&v)[PAIRS]) {
+    if (vec && bits == all_steps<2 * PAIRS>) {
         store_vectors(row, t0, v);
     } else {
 #pragma unroll
-        for (int e = 0; e < 2 * PAIRS; ++e)
-            if (t0 + e >= 0 && t0 + e < n) row[t0 + e] = IoTraits<IO>::from_f32(step_of(v, e));
+        for (int k = 0; k < PAIRS; ++k) {
+            IO* to = row + t0 + 2 * k;
+            const unsigned two = bits >> (2 * k) & 3;
+            if (sizeof(IO) == 2 && vec && two == 3) {
+                *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(v[k].x, v[k].y);
+            } else {
+                if (two & 1) to[0] = IoTraits<IO>::from_f32(v[k].x);
+                if (two & 2) to[1] = IoTraits<IO>::from_f32(v[k].y);
+            }
+        }
+    }
+}
+
+// The steps outside the bits become `other`, given as a word of elements.  With the recurrence gate shut
+// (-inf) a step has a = 1 and no input, and with the rest 0 no gradient: it passes the state through.
+template <typename IO> constexpr uint32_t shut = sizeof(IO) == 2 ? 0xff80ff80u : 0xff800000u;
+
+// (A bias of +inf must not meet that -inf.)
+__device__ __forceinline__ float bounded(float v) { return v == v ? fminf(fmaxf(v, -3e38f), 3e38f) : v; }
+
+template <typename IO, int N>
+__device__ __forceinline__ void mask_steps(unsigned bits, Raw<IO, N>& g, uint32_t other) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(g.v);
+    constexpr int kPer = 4 / sizeof(IO);
+#pragma unroll
+    for (int k = 0; k < N / kPer; ++k) {
+        const unsigned b = bits >> (k * kPer);
+        const uint32_t keep = kPer == 1 ? 0u - (b & 1) : (b & 1 ? 0xffffu : 0u) | (b & 2 ? 0xffff0000u : 0u);
+        w[k] = (w[k] & keep) | (other & ~keep);
     }
 }
 
@@ -385,6 +428,7 @@ __device__ __forceinline__ unsigned long long reset_flags(const unsigned char* r
     const unsigned char* q = row + t0;
     const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(q) & 7u);
     unsigned long long flags = 0;
+    if (t0 >= len || t0 + 8 <= 0) return 0;
     if (t0 >= 0 && t0 + 8 <= len && q - off >= begin && q - off + 16 <= end) {
         const auto* w = reinterpret_cast<const unsigned long long*>(q - off);
         flags = w[0] >> (8 * off);

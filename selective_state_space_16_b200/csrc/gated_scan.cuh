@@ -5,7 +5,8 @@
 // there.  The backward does the same from the last tile to the first; the states come from the
 // checkpoints, one before every group, so it has to scan in one direction only.
 //
-// SEG = 32: a warp per row.  SEG = 8, 2: several short rows per warp, so that few lanes idle.
+// SEG = 32: a warp per row.  SEG = 0: p.seg lanes per row, 1 to 16: several short rows per warp, so that few
+// lanes idle.
 // SPLIT: p.split warps of a block share one row, each taking every p.split-th tile; a barrier a round
 // joins their pairs.  That is for few long rows, which could not fill the GPU's warps otherwise.
 #pragma once
@@ -62,14 +63,15 @@ __device__ __forceinline__ float product(float2 (&a)[PAIRS]) {
 // The row of this lane, and where in it the lane works.
 template <int SEG, bool SPLIT>
 struct RowPlace {
-    long long row;
-    int lane;         // 0 .. SEG - 1
+    unsigned row;
+    int seg, lane;    // lanes per row; 0 .. seg - 1
     int part, parts;  // which of the warps that share the row
     __device__ RowPlace(const GatedParams& p) {
-        lane = threadIdx.x % SEG;
+        seg = SEG ? SEG : p.seg;
+        lane = threadIdx.x & (seg - 1);
         part = SPLIT ? threadIdx.x / 32 : 0;
         parts = SPLIT ? p.split : 1;
-        row = SPLIT ? blockIdx.x : static_cast<long long>(blockIdx.x) * (kGatedWarps * 32 / SEG) + threadIdx.x / SEG;
+        row = SPLIT ? blockIdx.x : blockIdx.x * (kGatedWarps * 32 / seg) + threadIdx.x / seg;
     }
 };
 
@@ -96,28 +98,27 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     const RowPlace<SEG, SPLIT> at(p);
     const long long row = at.row;
     const long long rows = static_cast<long long>(p.batch) * p.dim;
-    const bool valid = row < rows;
+    const bool valid = at.row < static_cast<unsigned>(rows);
     if (SEG == 32 && !valid) return;  // (a whole warp)
-    const int b = valid ? static_cast<int>(row / p.dim) : 0, d = valid ? static_cast<int>(row % p.dim) : 0;
+    const int b = valid ? at.row / static_cast<unsigned>(p.dim) : 0, d = valid ? at.row - static_cast<unsigned>(b) * p.dim : 0;
     const int len = valid ? row_length(p, b) : 0;
-    const IO* in[kIn] = {row_of<IO>(p.x, b, d), row_of<IO>(p.r, b, d), row_of<IO>(p.i, b, d)};
-    const IO* zrow[1] = {GATE ? row_of<IO>(p.z, b, d) : nullptr};
+    Reach reach{-15, 15};
+    const IO* in[kIn] = {row_in<IO>(p.x, b, d, reach), row_in<IO>(p.r, b, d, reach), row_in<IO>(p.i, b, d, reach)};
+    const IO* zrow[1] = {GATE ? row_in<IO>(p.z, b, d, reach) : nullptr};
+    reach.high += p.L;
     IO* y = p.y.p ? row_of<IO>(p.y, b, d) : nullptr;
     const int phase = phase_of(in[0]);
     bool vec[kIn], all_vec = true;
 #pragma unroll
     for (int k = 0; k < kIn; ++k) all_vec &= vec[k] = phase_of(in[k]) == phase;
-    Reach reach{-15, 15};
-    for (const GatedTensor* q : {&p.x, &p.r, &p.i}) narrow(reach, *q, b, d, p.batch, p.dim);
-    if (GATE) narrow(reach, p.z, b, d, p.batch, p.dim);
-    reach.high += p.L;
     const bool vy = phase_of(y) == phase, vz[1] = {phase_of(zrow[0]) == phase};
     const unsigned char* reset = RESET ? p.reset + static_cast<long long>(b) * p.L : nullptr;
     const unsigned char* reset_end = RESET ? p.reset + static_cast<long long>(p.batch) * p.L : nullptr;
     const float root = sqrtf(2.f * p.c * softplus_lam(p.lam[d]));
     const bool near = root <= kNear;
-    const float rb = -kLog2e * (p.r_bias ? p.r_bias[d] : 0.f), ib = -kLog2e * (p.i_bias ? p.i_bias[d] : 0.f);
+    const float rb = bounded(-kLog2e * (p.r_bias ? p.r_bias[d] : 0.f)), ib = -kLog2e * (p.i_bias ? p.i_bias[d] : 0.f);
     float carry = p.h0 && valid ? p.h0[row] : 0.f;
+    const float first = carry;
     float* ckpt = p.ckpt ? p.ckpt + sizeof(CkptHeader) / 4 + row * p.ckpt_row : nullptr;
     if (p.ckpt && blockIdx.x == 0 && threadIdx.x == 0) {
         constexpr unsigned n = 16 / sizeof(IO);
@@ -126,8 +127,8 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     }
 
     constexpr bool kAhead = sizeof(IO) == 2 || F32_AHEAD;
-    int t0 = (at.part * SEG + at.lane) * N - phase;
-    const int stride = at.parts * SEG * N;
+    int t0 = (at.part * at.seg + at.lane) * N - phase;
+    const int stride = at.parts * at.seg * N;
     Raw<IO, N> next[kIn];
     if (kAhead) load_steps(in, vec, all_vec, t0, valid ? p.L : 0, reach, next);  // (not waiting for len)
     int round = 0;
@@ -135,6 +136,8 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     for (int t = -phase; SEG == 32 ? t < len : __any_sync(kAll, t < len); t += stride, t0 += stride, ++round) {
         float2 a[kPairs], u[kPairs], v[kPairs], w[kPairs];
         if (!kAhead) load_steps(in, vec, all_vec, t0, len, reach, next);
+        const unsigned inside = steps_inside<N>(t0, len);
+        if (inside != all_steps<N>) mask_steps<IO, N>(inside, next[0], 0), mask_steps<IO, N>(inside, next[1], shut<IO>), mask_steps<IO, N>(inside, next[2], 0);
         unpack<IO, N>(next[0], u);
         unpack<IO, N>(next[1], v);
         unpack<IO, N>(next[2], w);
@@ -167,11 +170,6 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
                     if (flag_of(flags[e / 8], e % 8)) step_of(a, e) = kCut, step_of(u, e) = step_of(v, e);
             }
         }
-        if (t0 < 0 || t0 + N > len) {
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                if (t0 + e < 0 || t0 + e >= len) step_of(a, e) = 1.f, step_of(u, e) = 0.f;
-        }
         float P, H;
         const auto compose = [&](auto cut_tag) {  // (P, H) of the tile up to and with this lane's steps
             constexpr bool CUT = decltype(cut_tag)::value;
@@ -180,8 +178,8 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
             for (int e = 1; e < N; ++e) H = carry_on<CUT>(step_of(a, e), H, step_of(u, e));
             P = product<CUT>(a);
 #pragma unroll
-            for (int s = 1; s < SEG; s *= 2) {
-                const float Pe = __shfl_up_sync(kAll, P, s, SEG), He = __shfl_up_sync(kAll, H, s, SEG);
+            for (int s = 1; s < at.seg; s *= 2) {
+                const float Pe = __shfl_up_sync(kAll, P, s, at.seg), He = __shfl_up_sync(kAll, H, s, at.seg);
                 if (at.lane >= s) H = carry_on<CUT>(P, He, H), P = join<CUT>(P, Pe);
             }
         };
@@ -199,9 +197,9 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         const auto states = [&](auto cut_tag) {
             constexpr bool CUT = decltype(cut_tag)::value;
             const float all = carry_on<CUT>(P, enters, H);  // the state after this lane's steps
-            float h = __shfl_up_sync(kAll, all, 1, SEG);
+            float h = __shfl_up_sync(kAll, all, 1, at.seg);
             if (at.lane == 0) h = enters;
-            if (!SPLIT) carry = __shfl_sync(kAll, all, SEG - 1, SEG);
+            if (!SPLIT) carry = __shfl_sync(kAll, all, at.seg - 1, at.seg);
             if (ckpt && t0 < len) ckpt[(t0 + phase) / kGroup] = h;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
@@ -218,9 +216,9 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) u[k] = __fmul2_rn(u[k], gate_silu2<IO>(w[k]));
         }
-        if (y) store_steps(y, t0, len, vy, u);
+        if (y) store_steps(y, t0, inside, vy, u);
     }
-    if (p.last && valid && at.part == 0 && at.lane == 0) p.last[row] = carry;
+    if (p.last && valid && at.part == 0 && at.lane == 0) p.last[row] = len > 0 ? carry : first;
 }
 
 template <typename IO, bool GATE, bool RESET, int SEG, bool SPLIT>
@@ -231,13 +229,15 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     const RowPlace<SEG, SPLIT> at(p);
     const long long row = at.row;
     const long long rows = static_cast<long long>(p.batch) * p.dim;
-    const bool valid = row < rows;
+    const bool valid = at.row < static_cast<unsigned>(rows);
     if (SEG == 32 && !valid) return;
-    const int b = valid ? static_cast<int>(row / p.dim) : 0, d = valid ? static_cast<int>(row % p.dim) : 0;
+    const int b = valid ? at.row / static_cast<unsigned>(p.dim) : 0, d = valid ? at.row - static_cast<unsigned>(b) * p.dim : 0;
     const int len = valid ? row_length(p, b) : 0, L = valid ? p.L : 0;
-    const IO* in[kIn] = {row_of<IO>(p.x, b, d), row_of<IO>(p.r, b, d), row_of<IO>(p.i, b, d), row_of<IO>(p.dy, b, d)};
+    Reach reach{-15, 15};
+    const IO* in[kIn] = {row_in<IO>(p.x, b, d, reach), row_in<IO>(p.r, b, d, reach), row_in<IO>(p.i, b, d, reach), row_in<IO>(p.dy, b, d, reach)};
     IO* out[kOut] = {row_of<IO>(p.dx, b, d), row_of<IO>(p.dr, b, d), row_of<IO>(p.di, b, d)};
-    if (GATE) in[kIn - 1] = row_of<IO>(p.z, b, d), out[kOut - 1] = row_of<IO>(p.dz, b, d);
+    if (GATE) in[kIn - 1] = row_in<IO>(p.z, b, d, reach), out[kOut - 1] = row_of<IO>(p.dz, b, d);
+    reach.high += p.L;
     const CkptHeader where = *reinterpret_cast<const CkptHeader*>(p.ckpt);
     const int phase = static_cast<int>((where.base + b * where.bs + d * where.ds) % (16 / sizeof(IO)));
     bool vin[kIn], vout[kOut], all_vec = true;
@@ -245,32 +245,29 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     for (int k = 0; k < kIn; ++k) all_vec &= vin[k] = phase_of(in[k]) == phase;
 #pragma unroll
     for (int k = 0; k < kOut; ++k) all_vec &= vout[k] = phase_of(out[k]) == phase;
-    Reach reach{-15, 15};
-    for (const GatedTensor* q : {&p.x, &p.r, &p.i, &p.dy}) narrow(reach, *q, b, d, p.batch, p.dim);
-    if (GATE) narrow(reach, p.z, b, d, p.batch, p.dim);
-    reach.high += p.L;
     const unsigned char* reset = RESET ? p.reset + static_cast<long long>(b) * p.L : nullptr;
     const unsigned char* reset_end = RESET ? p.reset + static_cast<long long>(p.batch) * p.L : nullptr;
     const float* ckpt = p.ckpt + sizeof(CkptHeader) / 4 + row * p.ckpt_row;
     const float root = sqrtf(2.f * p.c * softplus_lam(p.lam[d]));
     const bool near = root <= kNear;
-    const float rb = -kLog2e * (p.r_bias ? p.r_bias[d] : 0.f), ib = -kLog2e * (p.i_bias ? p.i_bias[d] : 0.f);
+    const float rb = bounded(-kLog2e * (p.r_bias ? p.r_bias[d] : 0.f)), ib = -kLog2e * (p.i_bias ? p.i_bias[d] : 0.f);
     float carry = p.dlast && valid ? p.dlast[row] : 0.f;  // a_{t+1} g_{t+1}: what the steps after the tile send back
+    const float first = carry;
     float2 sumT = both(0.f), sumr = both(0.f), sumi = both(0.f);
 
-    const int stride = at.parts * SEG * N;
+    const int stride = at.parts * at.seg * N;
     int t = (len + phase + stride - 1) / stride * stride - phase;  // where the rounds with steps end
-    for (int t0 = t + (at.part * SEG + at.lane) * N; t0 < L; t0 += stride) {  // padding: zeros
+    for (int t0 = t + (at.part * at.seg + at.lane) * N; t0 < L; t0 += stride) {  // padding: zeros
         float2 zero[kPairs] = {};
 #pragma unroll
-        for (int k = 0; k < kOut; ++k) store_steps(out[k], t0, L, vout[k], zero);
+        for (int k = 0; k < kOut; ++k) store_steps(out[k], t0, steps_inside<N>(t0, L), vout[k], zero);
     }
     using In = Ring<IO, N, kIn>;
     constexpr int kStages = kBwdStages<IO>;
     extern __shared__ uint4 ring[];
     float* states_in = reinterpret_cast<float*>(ring + kStages * In::kVecs * blockDim.x) + threadIdx.x;  // the checkpoints' slots
     const auto load = [&](int stage, int t) {
-        const int t0 = t + (at.part * SEG + at.lane) * N;
+        const int t0 = t + (at.part * at.seg + at.lane) * N;
         const bool active = t >= -phase;
         if (active && t0 < len) cp_async_4(states_in + stage * blockDim.x, ckpt + (t0 + phase) / kGroup);
         In::load(ring, stage, in, vin, all_vec, t0, active ? len : -N, reach);
@@ -280,11 +277,12 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     for (int k = 0; k < kStages - 1; ++k) load(k, t - (k + 1) * stride);
 #pragma unroll 1
     for (t -= stride; SEG == 32 ? t >= -phase : __any_sync(kAll, t >= -phase); t -= stride, ++round) {
-        const int t0 = t + (at.part * SEG + at.lane) * N;
+        const int t0 = t + (at.part * at.seg + at.lane) * N;
         // (a short row that is done while others of its warp go on lies before its first step: no steps inside)
         const bool active = SEG == 32 || t >= -phase;
         const int end = active ? len : -phase;
-        const bool whole = t0 >= 0 && t0 + N <= end;
+        const unsigned inside = steps_inside<N>(t0, end);
+        const bool whole = inside == all_steps<N>;
         float2 a[kPairs], g[kPairs], kx[kPairs], ki[kPairs], kT[kPairs], kr[kPairs], b[kPairs], ax[kPairs];
         Raw<IO, N> raw[kIn];
         float h = 0.f;
@@ -298,6 +296,10 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         } else {
             if (t0 < end && active) h = ckpt[(t0 + phase) / kGroup];
             load_steps(in, vin, all_vec, t0, active ? end : -N, reach, raw);
+        }
+        if (!whole) {
+#pragma unroll
+            for (int k = 0; k < kIn; ++k) mask_steps<IO, N>(inside, raw[k], k == 1 ? shut<IO> : 0);
         }
         unpack<IO, N>(raw[0], kx);
         unpack<IO, N>(raw[1], kr);
@@ -336,14 +338,6 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
             coefficients(std::true_type{});
         else
             coefficients(std::false_type{});
-        if (!whole) {
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                if (t0 + e < 0 || t0 + e >= end) {
-                    step_of(a, e) = 1.f;
-                    step_of(g, e) = step_of(kT, e) = step_of(ax, e) = step_of(kr, e) = step_of(ki, e) = step_of(kx, e) = step_of(b, e) = 0.f;
-                }
-        }
         const auto states = [&](auto cut_tag) {
             constexpr bool CUT = decltype(cut_tag)::value;
 #pragma unroll
@@ -375,14 +369,10 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
                 b[k] = __fmul2_rn(__fmul2_rn(g[k], b[k]), slope);
                 g[k] = __fmul2_rn(g[k], zs);
             }
-            if (all_vec && whole) {
+            if (all_vec && whole)
                 store_vectors(out[kOut - 1], t0, b);
-            } else {
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                    if (t0 + e < 0 || t0 + e >= end) step_of(g, e) = step_of(b, e) = 0.f;
-                if (active) store_steps(out[kOut - 1], t0, L, vout[kOut - 1], b);
-            }
+            else if (active)
+                store_steps(out[kOut - 1], t0, steps_inside<N>(t0, L), vout[kOut - 1], b);
         }
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) ax[k] = __fmul2_rn(a[k], g[k]);
@@ -394,9 +384,9 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
             for (int e = N - 2; e >= 0; --e) S = carry_on<CUT>(step_of(a, e), S, step_of(ax, e));
             P = product<CUT>(a);
 #pragma unroll
-            for (int s = 1; s < SEG; s *= 2) {
-                const float Pl = __shfl_down_sync(kAll, P, s, SEG), Sl = __shfl_down_sync(kAll, S, s, SEG);
-                if (at.lane + s < SEG) S = carry_on<CUT>(P, Sl, S), P = join<CUT>(P, Pl);
+            for (int s = 1; s < at.seg; s *= 2) {
+                const float Pl = __shfl_down_sync(kAll, P, s, at.seg), Sl = __shfl_down_sync(kAll, S, s, at.seg);
+                if (at.lane + s < at.seg) S = carry_on<CUT>(P, Sl, S), P = join<CUT>(P, Pl);
             }
         };
         const auto drop = [&] {  // a reset's own gradient goes nowhere either, not even as 0 * inf
@@ -418,9 +408,9 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         const auto gradients = [&](auto cut_tag) {
             constexpr bool CUT = decltype(cut_tag)::value;
             const float all = carry_on<CUT>(P, enters, S);
-            float s = __shfl_down_sync(kAll, all, 1, SEG);
-            if (at.lane == SEG - 1) s = enters;
-            if (!SPLIT) carry = __shfl_sync(kAll, all, 0, SEG);
+            float s = __shfl_down_sync(kAll, all, 1, at.seg);
+            if (at.lane == at.seg - 1) s = enters;
+            if (!SPLIT) carry = __shfl_sync(kAll, all, 0, at.seg);
 #pragma unroll
             for (int e = N - 1; e >= 0; --e) {
                 step_of(g, e) += s;
@@ -448,20 +438,21 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         } else if (active) {
 #pragma unroll
             for (int e = 0; e < N; ++e)  // (0 times an infinite gradient of the last state)
-                if (t0 + e >= end) step_of(kx, e) = step_of(kr, e) = step_of(ki, e) = 0.f;
-            store_steps(out[0], t0, L, vout[0], kx);
-            store_steps(out[1], t0, L, vout[1], kr);
-            store_steps(out[2], t0, L, vout[2], ki);
+                if (!(inside >> e & 1)) step_of(kx, e) = step_of(kr, e) = step_of(ki, e) = 0.f;
+            const unsigned to = steps_inside<N>(t0, L);
+            store_steps(out[0], t0, to, vout[0], kx);
+            store_steps(out[1], t0, to, vout[1], kr);
+            store_steps(out[2], t0, to, vout[2], ki);
         }
     }
-    if (p.dh0 && valid && at.part == 0 && at.lane == 0) p.dh0[row] = carry;
+    if (p.dh0 && valid && at.part == 0 && at.lane == 0) p.dh0[row] = len > 0 ? carry : first;
     if (p.part) {
         float sT = sumT.x + sumT.y, sr = sumr.x + sumr.y, si = sumi.x + sumi.y;
 #pragma unroll
-        for (int s = SEG / 2; s; s /= 2) {
-            sT += __shfl_xor_sync(kAll, sT, s, SEG);
-            sr += __shfl_xor_sync(kAll, sr, s, SEG);
-            si += __shfl_xor_sync(kAll, si, s, SEG);
+        for (int s = at.seg / 2; s; s /= 2) {
+            sT += __shfl_xor_sync(kAll, sT, s, at.seg);
+            sr += __shfl_xor_sync(kAll, sr, s, at.seg);
+            si += __shfl_xor_sync(kAll, si, s, at.seg);
         }
         if constexpr (SPLIT) {
             if (at.lane == 0) part_sums[0][at.part] = sT, part_sums[1][at.part] = sr, part_sums[2][at.part] = si;
