@@ -77,7 +77,7 @@ ssm_status_t launch_move(const CacheMove& m, long long pairs, int sm_count, cuda
     const long long total = m.units * pairs;
     if (total == 0) return SSM_OK;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(total, 8LL * sm_count)));
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(total, static_cast<long long>(ssm::kMoveBlocksPerSm) * sm_count)));
     cfg.blockDim = dim3(ssm::kMoveThreads);
     cfg.stream = s;
     cudaLaunchAttribute pdl{};
