@@ -225,10 +225,11 @@ ssm_status_t ssm_gated_state_update(const ssm_gated_step_t* args, ssm_stream_t s
                           static_cast<const void*>(a.r_bias), static_cast<const void*>(a.i_bias)})
         if (!float_aligned(q)) return SSM_ERR_INVALID_ARG;
     if (a.batch > 65535) return SSM_ERR_UNSUPPORTED;  // the batch row is a grid y index
-    const ssm_status_t st = check_device(nullptr);
+    int sms = 0;
+    const ssm_status_t st = check_device(&sms);
     if (st != SSM_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return a.io_dtype == SSM_BF16 ? launch_gated_step<__nv_bfloat16>(a, s) : launch_gated_step<float>(a, s);
+    return a.io_dtype == SSM_BF16 ? launch_gated_step<__nv_bfloat16>(a, sms, s) : launch_gated_step<float>(a, sms, s);
 }
 
 }  // extern "C"

@@ -1,6 +1,8 @@
 // gated_launch.cuh -- launch shapes of the gated recurrence's kernels.
 #pragma once
 
+#include <algorithm>
+
 #include "gated_host.h"
 #include "gated_scan.cuh"
 #include "gated_step.cuh"
@@ -63,7 +65,7 @@ ssm_status_t launch_gated_bwd(const ssm::GatedParams& p, cudaStream_t stream) {
 }
 
 template <typename IO>
-ssm_status_t launch_gated_step(const ssm_gated_step_t& a, cudaStream_t stream) {
+ssm_status_t launch_gated_step(const ssm_gated_step_t& a, int sms, cudaStream_t stream) {
     const unsigned mask = ssm::kStepChannels * sizeof(IO) - 1;
     const auto on = [](const void* p, long long stride, unsigned m) {
         return ((reinterpret_cast<uintptr_t>(p) | static_cast<unsigned long long>(stride)) & m) == 0;
@@ -73,12 +75,15 @@ ssm_status_t launch_gated_step(const ssm_gated_step_t& a, cudaStream_t stream) {
                      io(a.y, a.y_stride) && on(a.state, a.state_stride * 4, 15) && on(a.lam, 0, 15) && on(a.r_bias, 0, 15) &&
                      on(a.i_bias, 0, 15);
     const int per_block = ssm::kStepThreads * ssm::kStepChannels;
-    const dim3 grid(static_cast<unsigned>((a.dim + per_block - 1) / per_block), static_cast<unsigned>(a.batch));
-    const ssm::GatedStep g{a, vec};
-    if (a.z)
-        ssm::gated_step_kernel<IO, true><<<grid, ssm::kStepThreads, 0, stream>>>(g);
-    else
-        ssm::gated_step_kernel<IO, false><<<grid, ssm::kStepThreads, 0, stream>>>(g);
+    const int chunks = (a.dim + per_block - 1) / per_block;
+    // rows of a block: as few as fill the resident blocks
+    const int rows = static_cast<int>(std::min<long long>(a.batch, std::max<long long>(1, STEP_BLOCKS * sms / chunks)));
+    const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(rows));
+    const long long bitmap = (a.n_slots + 31LL) / 32 * 4;
+    const bool small = bitmap <= 40 * 1024;
+    const ssm::GatedStep g{a, vec, !small};
+    auto kern = a.z ? ssm::gated_step_kernel<IO, true> : ssm::gated_step_kernel<IO, false>;
+    kern<<<grid, ssm::kStepThreads, a.slots && a.batch > 1 && small ? static_cast<int>(bitmap) : 0, stream>>>(g);
     return launch_status();
 }
 
