@@ -99,8 +99,8 @@ bool is_input(const ssm_gated_args_t* a, const void* q) {
     return q && (q == a->x.data || q == a->r.data || q == a->i.data || q == a->z.data);
 }
 
-ssm_status_t launch_fwd(int io, const GatedParams& p, cudaStream_t s) {
-    return io == SSM_BF16 ? launch_gated_fwd<__nv_bfloat16>(p, s) : launch_gated_fwd<float>(p, s);
+ssm_status_t launch_fwd(int io, const GatedParams& p, int sms, cudaStream_t s) {
+    return io == SSM_BF16 ? launch_gated_fwd<__nv_bfloat16>(p, sms, s) : launch_gated_fwd<float>(p, sms, s);
 }
 
 }  // namespace
@@ -124,7 +124,8 @@ ssm_status_t ssm_gated_scan_fwd(const ssm_gated_args_t* args, ssm_gated_out_t y,
     p.y = tensor(y, p.batch, p.dim);
     if (rows && p.L > 0 && !rows_apart(p.y, p.batch, p.dim, p.L)) return SSM_ERR_INVALID_ARG;
     if (!rows) return SSM_OK;
-    st = check_device(nullptr);
+    int sms = 0;
+    st = check_device(&sms);
     if (st != SSM_OK) return st;
     if (p.L == 0) {  // no steps (and, with torch, no addresses): the state passes through
         const size_t bytes = static_cast<size_t>(p.batch) * p.dim * sizeof(float);
@@ -136,7 +137,7 @@ ssm_status_t ssm_gated_scan_fwd(const ssm_gated_args_t* args, ssm_gated_out_t y,
     }
     p.last = last_state;
     p.ckpt = static_cast<float*>(checkpoints);
-    return launch_fwd(args->io_dtype, p, reinterpret_cast<cudaStream_t>(stream));
+    return launch_fwd(args->io_dtype, p, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t ssm_gated_bwd_workspace_size(int batch, int dim, int64_t seqlen, int have_checkpoints) {
@@ -187,7 +188,8 @@ ssm_status_t ssm_gated_scan_bwd(const ssm_gated_args_t* args, const ssm_gated_gr
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
         workspace_bytes < ssm_gated_bwd_workspace_size(p.batch, p.dim, p.L, checkpoints != nullptr))
         return SSM_ERR_WORKSPACE;
-    st = check_device(nullptr);
+    int sms = 0;
+    st = check_device(&sms);
     if (st != SSM_OK) return st;
     p.dlast = g.dlast_state;
     p.part = sums ? static_cast<float*>(workspace) : nullptr;
@@ -197,11 +199,11 @@ ssm_status_t ssm_gated_scan_bwd(const ssm_gated_args_t* args, const ssm_gated_gr
                                           round_up(static_cast<size_t>(p.batch) * p.dim * 3 * sizeof(float), 256));
         GatedParams f = p;  // a forward that stores nothing but the checkpoints
         f.z.p = nullptr;
-        st = launch_fwd(args->io_dtype, f, s);
+        st = launch_fwd(args->io_dtype, f, sms, s);
         if (st != SSM_OK) return st;
     }
     p.dh0 = g.dinitial_state;
-    st = args->io_dtype == SSM_BF16 ? launch_gated_bwd<__nv_bfloat16>(p, s) : launch_gated_bwd<float>(p, s);
+    st = args->io_dtype == SSM_BF16 ? launch_gated_bwd<__nv_bfloat16>(p, sms, s) : launch_gated_bwd<float>(p, sms, s);
     if (st != SSM_OK || !sums) return st;
     gated_bwd_params_kernel<<<static_cast<unsigned>((p.dim + 127) / 128), 128, 0, s>>>(p.part, p.lam, g.dlam, g.dr_bias,
                                                                                        g.di_bias, p.batch, p.dim);

@@ -10,21 +10,40 @@
 
 namespace ssmh {
 
-// How rows are laid on lanes, each of which holds `steps` steps.  Rows that fit in half a warp share one;
-// few long rows are split over the warps of a block until the GPU has work for all its SMs.
+// How rows are laid on lanes, each of which holds `steps` steps: rows that fit in half a warp share one; a
+// long row is split over `split` warps in `blocks` blocks of a cluster.
 struct GatedShape {
-    int seg, split;
+    int seg, split, blocks;
 };
 
+// Splitting goes on, by twos, until the GPU has 8 warps per SM (16 are resident) or a round covers the
+// row: up to 4 warps of one block, then with fewer rows than SMs up to 8 blocks, else up to 8 warps.
+// Forward and backward of bf16 rows with a gate, us: 64 x 32768 60 with 4 warps, 44 with 16 in a block, 33
+// with 4 x 8 blocks; 128 x 32768 61, 47 and 47 (4 x 4); 200 x 16384 45 with 4, 43 with 8, 43 with 4 x 2 blocks;
+// 300 x 16384 53 with 4, 57 with 8, 64 with 4 x 2; 768 x 16384 121, 92, 92 and 100 with 1, 2, 4 and 8; 1536 x 8192
+// 86 and 93 with 1 and 2.  3 or 6 warps took longer than 2 and 4 throughout.
+inline GatedShape split_shape(long long rows, int L, int steps, int sms) {
+    const long long tiles = (L + 32LL * steps - 1) / (32 * steps);
+    int warps = 1, blocks = 1;
+    while (rows * warps * blocks < 8LL * sms && warps * blocks < tiles) {
+        if (warps < 4 || (rows >= sms && warps < 8))
+            warps *= 2;
+        else if (rows < sms && blocks < ssm::kMaxCluster)
+            blocks *= 2;
+        else
+            break;
+    }
+    return {32, warps * blocks, blocks};
+}
+
 template <typename IO>
-GatedShape gated_shape(long long rows, int L, int steps) {
+GatedShape gated_shape(long long rows, int L, int steps, int sms) {
     constexpr int kVec = 16 / sizeof(IO);
     const long long need = L % kVec ? L + static_cast<long long>(kVec) - 1 : L;  // (rows then start anywhere in a vector)
-    int seg = 1, split = 1;
+    int seg = 1;
     while (seg < 32 && static_cast<long long>(seg) * steps < need) seg *= 2;
-    if (seg == 32)
-        while (split < ssm::kMaxSplit && rows * split < 148 * 10 && static_cast<long long>(split) * 32 * steps < L) split *= 2;
-    return {seg, split};
+    if (seg < 32) return {seg, 1, 1};
+    return split_shape(rows, L, steps, sms);
 }
 
 using GatedKernel = void (*)(const ssm::GatedParams);
@@ -37,31 +56,42 @@ GatedKernel gated_kernel(GatedShape shape, bool backward) {
 }
 
 template <typename IO>
-ssm_status_t launch_gated(ssm::GatedParams p, bool backward, cudaStream_t stream) {
+ssm_status_t launch_gated(ssm::GatedParams p, bool backward, int sms, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.batch) * p.dim;
-    const GatedShape shape = gated_shape<IO>(rows, p.L, backward ? ssm::kBwdSteps : ssm::kFwdSteps<IO>);
+    const GatedShape shape = gated_shape<IO>(rows, p.L, backward ? ssm::kBwdSteps : ssm::kFwdSteps<IO>, sms);
     p.seg = shape.seg;
     p.split = shape.split;
+    p.blocks = static_cast<unsigned>(shape.blocks);
     const bool gate = p.z.p != nullptr, reset = p.reset != nullptr;
     const GatedKernel kern = gate ? (reset ? gated_kernel<IO, true, true>(shape, backward) : gated_kernel<IO, true, false>(shape, backward))
                                   : (reset ? gated_kernel<IO, false, true>(shape, backward) : gated_kernel<IO, false, false>(shape, backward));
-    const int block = shape.split > 1 ? shape.split * 32 : ssm::kGatedWarps * 32;
-    const long long per_block = shape.split > 1 ? 1 : block / shape.seg;
+    const int block = shape.split > 1 ? shape.split / shape.blocks * 32 : ssm::kGatedWarps * 32;
+    const long long per_block = block / shape.seg;
     const int smem = backward ? ssm::bwd_smem<IO>(gate, block) : 0;
     if (smem > 46 * 1024 &&  // (with the static part of it, past the 48 KB that need no asking)
         !ensure_smem_attr(reinterpret_cast<const void*>(kern), smem)) return SSM_ERR_LAUNCH;
-    kern<<<static_cast<unsigned>((rows + per_block - 1) / per_block), block, smem, stream>>>(p);
-    return launch_status();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(shape.split > 1 ? rows * shape.blocks : (rows + per_block - 1) / per_block));
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute cluster{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = static_cast<unsigned>(shape.blocks);
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = shape.blocks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? launch_status() : SSM_ERR_LAUNCH;
 }
 
 template <typename IO>
-ssm_status_t launch_gated_fwd(const ssm::GatedParams& p, cudaStream_t stream) {
-    return launch_gated<IO>(p, false, stream);
+ssm_status_t launch_gated_fwd(const ssm::GatedParams& p, int sms, cudaStream_t stream) {
+    return launch_gated<IO>(p, false, sms, stream);
 }
 
 template <typename IO>
-ssm_status_t launch_gated_bwd(const ssm::GatedParams& p, cudaStream_t stream) {
-    return launch_gated<IO>(p, true, stream);
+ssm_status_t launch_gated_bwd(const ssm::GatedParams& p, int sms, cudaStream_t stream) {
+    return launch_gated<IO>(p, true, sms, stream);
 }
 
 template <typename IO>

@@ -32,6 +32,7 @@ struct GatedParams {
     float c;
     int seg;    // lanes that share a row
     int split;  // warps that share a row (1: a row per warp or part of one)
+    unsigned blocks;  // and the blocks that they belong to, a cluster
     // backward
     GatedTensor dy, dx, dr, di, dz;
     const float* dlast;

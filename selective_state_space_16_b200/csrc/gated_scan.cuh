@@ -7,8 +7,10 @@
 //
 // SEG = 32: a warp per row.  SEG = 0: p.seg lanes per row, 1 to 16: several short rows per warp, so that few
 // lanes idle.
-// SPLIT: p.split warps of a block share one row, each taking every p.split-th tile; a barrier a round
-// joins their pairs.  That is for few long rows, which could not fill the GPU's warps otherwise.
+// SPLIT: the warps of a block, or of a cluster of blocks, share one row: of p.split warps in all each takes
+// every p.split-th tile, and a barrier a round joins their pairs, which every warp writes into the
+// shared memory of all blocks of the cluster.  That is for few long rows, which could not fill the GPU's
+// warps otherwise.
 #pragma once
 
 #include <type_traits>
@@ -25,7 +27,9 @@ __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
 }
 
 constexpr int kGatedWarps = 4;  // warps of a block without SPLIT
-constexpr int kMaxSplit = 16;
+constexpr int kMaxSplit = 8;   // warps of a block with SPLIT
+constexpr int kMaxParts = 32;  // warps that share a row
+constexpr int kMaxCluster = 8;
 #ifndef FWD_MINB
 #define FWD_MINB 4
 #endif
@@ -60,18 +64,36 @@ __device__ __forceinline__ float product(float2 (&a)[PAIRS]) {
     }
 }
 
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Writes two floats to the same place of block `rank`'s shared memory as `here` in this one's.
+__device__ __forceinline__ void st_cluster(const float2* here, unsigned rank, float2 v) {
+    unsigned to;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(here)), "r"(rank));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(v.x), "f"(v.y) : "memory");
+}
+
 // The row of this lane, and where in it the lane works.
 template <int SEG, bool SPLIT>
 struct RowPlace {
     unsigned row;
     int seg, lane;    // lanes per row; 0 .. seg - 1
     int part, parts;  // which of the warps that share the row
+    unsigned blocks, rank;  // of the cluster that shares it
     __device__ RowPlace(const GatedParams& p) {
         seg = SEG ? SEG : p.seg;
         lane = threadIdx.x & (seg - 1);
-        part = SPLIT ? threadIdx.x / 32 : 0;
+        blocks = SPLIT ? p.blocks : 1;
+        rank = blocks > 1 ? cluster_rank() : 0;
+        part = SPLIT ? rank * (blockDim.x / 32) + threadIdx.x / 32 : 0;
         parts = SPLIT ? p.split : 1;
-        row = SPLIT ? blockIdx.x : blockIdx.x * (kGatedWarps * 32 / seg) + threadIdx.x / seg;
+        row = SPLIT ? blockIdx.x / blocks : blockIdx.x * (kGatedWarps * 32 / seg) + threadIdx.x / seg;
     }
 };
 
@@ -79,9 +101,17 @@ struct RowPlace {
 // other, what enters this warp's tile and, in `carry`, what leaves the round.  One barrier a round:
 // a buffer is written again two rounds later, behind the barrier that its readers have passed.
 template <bool RESET>
-__device__ __forceinline__ float join_parts(float2* pairs, int place, int parts, bool writer, float P, float H, float& carry) {
-    if (writer) pairs[place] = make_float2(P, H);
-    __syncthreads();
+__device__ __forceinline__ float join_parts(float2* pairs, int place, int parts, int blocks, int writer, float P, float H, float& carry) {
+    const int lane = threadIdx.x & 31;
+    if (blocks == 1) {
+        if (lane == writer) pairs[place] = make_float2(P, H);
+        __syncthreads();
+    } else {
+        const float2 v = make_float2(__shfl_sync(kAll, P, writer), __shfl_sync(kAll, H, writer));
+        if (lane < blocks) st_cluster(pairs + place, lane, v);
+        cluster_arrive();
+        cluster_wait();
+    }
     float in = carry, mine = carry;
     for (int k = 0; k < parts; ++k) {
         if (k == place) mine = in;
@@ -92,14 +122,15 @@ __device__ __forceinline__ float join_parts(float2* pairs, int place, int parts,
 }
 
 template <typename IO, bool GATE, bool RESET, int SEG, bool SPLIT>
-__global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPLIT ? 1 : FWD_MINB) gated_fwd_kernel(const GatedParams p) {
+__global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPLIT ? 2 : FWD_MINB) gated_fwd_kernel(const GatedParams p) {
     constexpr int N = kFwdSteps<IO>, kPairs = N / 2, kIn = 3;
-    __shared__ float2 pairs[SPLIT ? 2 : 1][SPLIT ? kMaxSplit : 1];
+    __shared__ float2 pairs[SPLIT ? 2 : 1][SPLIT ? kMaxParts : 1];
     const RowPlace<SEG, SPLIT> at(p);
     const long long row = at.row;
     const long long rows = static_cast<long long>(p.batch) * p.dim;
     const bool valid = at.row < static_cast<unsigned>(rows);
     if (SEG == 32 && !valid) return;  // (a whole warp)
+    if (SPLIT && at.blocks > 1) cluster_arrive(), cluster_wait();  // every block has begun: its shared memory may be written
     const int b = valid ? at.row / static_cast<unsigned>(p.dim) : 0, d = valid ? at.row - static_cast<unsigned>(b) * p.dim : 0;
     const int len = valid ? row_length(p, b) : 0;
     Reach reach{-15, 15};
@@ -191,7 +222,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         }
         float enters = carry;
         if constexpr (SPLIT) {
-            enters = join_parts<RESET>(pairs[round & 1], at.part, at.parts, at.lane == 31, any_cut ? kCut : P, H, carry);
+            enters = join_parts<RESET>(pairs[round & 1], at.part, at.parts, at.blocks, 31, any_cut ? kCut : P, H, carry);
             if (RESET && any_cut && !careful && !finite(enters)) careful = true, compose(std::true_type{});
         }
         const auto states = [&](auto cut_tag) {
@@ -222,15 +253,16 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
 }
 
 template <typename IO, bool GATE, bool RESET, int SEG, bool SPLIT>
-__global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPLIT ? 1 : (sizeof(IO) == 2 ? BWD_MINB : BWD_MINB32)) gated_bwd_kernel(const GatedParams p) {
+__global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPLIT ? 2 : (sizeof(IO) == 2 ? BWD_MINB : BWD_MINB32)) gated_bwd_kernel(const GatedParams p) {
     constexpr int N = kBwdSteps, kPairs = N / 2, kIn = GATE ? 5 : 4, kOut = GATE ? 4 : 3;
-    __shared__ float2 pairs[SPLIT ? 2 : 1][SPLIT ? kMaxSplit : 1];
-    __shared__ float part_sums[SPLIT ? 3 : 1][SPLIT ? kMaxSplit : 1];
+    __shared__ float2 pairs[SPLIT ? 2 : 1][SPLIT ? kMaxParts : 1];
+    __shared__ float2 part_sums[SPLIT ? kMaxParts : 1][2];
     const RowPlace<SEG, SPLIT> at(p);
     const long long row = at.row;
     const long long rows = static_cast<long long>(p.batch) * p.dim;
     const bool valid = at.row < static_cast<unsigned>(rows);
     if (SEG == 32 && !valid) return;
+    if (SPLIT && at.blocks > 1) cluster_arrive(), cluster_wait();
     const int b = valid ? at.row / static_cast<unsigned>(p.dim) : 0, d = valid ? at.row - static_cast<unsigned>(b) * p.dim : 0;
     const int len = valid ? row_length(p, b) : 0, L = valid ? p.L : 0;
     Reach reach{-15, 15};
@@ -402,7 +434,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         }
         float enters = carry;
         if constexpr (SPLIT) {
-            enters = join_parts<RESET>(pairs[round & 1], at.parts - 1 - at.part, at.parts, at.lane == 0, any_cut ? kCut : P, S, carry);
+            enters = join_parts<RESET>(pairs[round & 1], at.parts - 1 - at.part, at.parts, at.blocks, 0, any_cut ? kCut : P, S, carry);
             if (RESET && any_cut && !careful && !finite(enters)) careful = true, drop(), compose(std::true_type{});
         }
         const auto gradients = [&](auto cut_tag) {
@@ -454,13 +486,19 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
             sr += __shfl_xor_sync(kAll, sr, s, at.seg);
             si += __shfl_xor_sync(kAll, si, s, at.seg);
         }
-        if constexpr (SPLIT) {
-            if (at.lane == 0) part_sums[0][at.part] = sT, part_sums[1][at.part] = sr, part_sums[2][at.part] = si;
-            __syncthreads();
-            if (threadIdx.x < 3) {
-                float s = 0.f;
-                for (int k = 0; k < at.parts; ++k) s += part_sums[threadIdx.x][k];
-                p.part[threadIdx.x * rows + row] = s;
+        if constexpr (SPLIT) {  // summed by the first block, in the order of the parts
+            if (at.blocks == 1) {
+                if (at.lane == 0) part_sums[at.part][0] = make_float2(sT, sr), part_sums[at.part][1] = make_float2(si, 0.f);
+                __syncthreads();
+            } else {
+                if (at.lane == 0) st_cluster(&part_sums[at.part][0], 0, make_float2(sT, sr)), st_cluster(&part_sums[at.part][1], 0, make_float2(si, 0.f));
+                cluster_arrive();
+                cluster_wait();
+            }
+            if (at.rank == 0 && threadIdx.x == 0) {
+                float3 s = make_float3(0.f, 0.f, 0.f);
+                for (int k = 0; k < at.parts; ++k) s.x += part_sums[k][0].x, s.y += part_sums[k][0].y, s.z += part_sums[k][1].x;
+                p.part[row] = s.x, p.part[rows + row] = s.y, p.part[2 * rows + row] = s.z;
             }
         } else if (valid && at.lane == 0) {
             p.part[row] = sT, p.part[rows + row] = sr, p.part[2 * rows + row] = si;

@@ -129,10 +129,28 @@ def test_saturated_gates(cuda_device, io):
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
-@pytest.mark.parametrize("B,D,L", [(1, 1, 40000), (1, 3, 9001), (2, 700, 129), (1, 2500, 77), (40, 130, 60)])
+@pytest.mark.parametrize("B,D,L", [(1, 1, 40000), (1, 3, 9001), (2, 700, 129), (1, 2500, 77), (40, 130, 60), (2, 75, 2500), (1, 170, 5003),
+                                   (1, 90, 4100), (4, 150, 1030)])
 def test_shapes(cuda_device, io, B, D, L):
     t, dy, dlast = inputs(B, D, L, io, seed=B + D + L)
     compare(run_all(t, dy, dlast, True), t, dy, dlast, f"{B}x{D}x{L}")
+
+
+def test_rows_split_over_blocks_with_resets_and_lengths(cuda_device):
+    """Few rows, each shared by the warps of several blocks: documents, padding and non-finite values across them."""
+    B, D, L = 3, 5, 21000
+    t, dy, dlast = inputs(B, D, L, "bf16", lengths=[L, 9, 13001], reset=0.0003, seed=41)
+    compare(run_all(t, dy, dlast, True), t, dy, dlast, "split")
+    compare(run_all(t, dy, dlast, False), t, dy, dlast, "split, no checkpoints")
+    t["reset"][0, :] = 0
+    t["reset"][0, 4000] = t["reset"][0, 9000] = 1
+    t["x"][0, :, 100] = float("nan")
+    dy[0, :, 20000] = float("inf")
+    got = run_all(t, dy, dlast, True)
+    assert bool(torch.isfinite(got["y"][0, :, 4000:]).all()) and not bool(torch.isfinite(got["y"][0, 0, 101]))
+    for k in ("dx", "dr", "di", "dz"):
+        assert bool(torch.isfinite(got[k][0, :, 4000:9000]).all()) and bool(torch.isfinite(got[k][0, :, 20001:]).all()), k
+    assert not bool(torch.isfinite(got["dx"][0, 0, 19999]))
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
