@@ -61,7 +61,7 @@ ssm_status_t launch_gated(ssm::GatedParams p, bool backward, int sms, cudaStream
     const GatedShape shape = gated_shape<IO>(rows, p.L, backward ? ssm::kBwdSteps : ssm::kFwdSteps<IO>, sms);
     p.seg = shape.seg;
     p.split = shape.split;
-    p.blocks = static_cast<unsigned>(shape.blocks);
+    p.blocks = shape.blocks;
     const bool gate = p.z.p != nullptr, reset = p.reset != nullptr;
     const GatedKernel kern = gate ? (reset ? gated_kernel<IO, true, true>(shape, backward) : gated_kernel<IO, true, false>(shape, backward))
                                   : (reset ? gated_kernel<IO, false, true>(shape, backward) : gated_kernel<IO, false, false>(shape, backward));
@@ -107,7 +107,7 @@ ssm_status_t launch_gated_step(const ssm_gated_step_t& a, int sms, cudaStream_t 
     const int per_block = ssm::kStepThreads * ssm::kStepChannels;
     const int chunks = (a.dim + per_block - 1) / per_block;
     // rows of a block: as few as fill the resident blocks
-    const int rows = static_cast<int>(std::min<long long>(a.batch, std::max<long long>(1, STEP_BLOCKS * sms / chunks)));
+    const int rows = static_cast<int>(std::min<long long>(a.batch, std::max<long long>(1, ssm::kStepBlocks * sms / chunks)));
     const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(rows));
     const long long bitmap = (a.n_slots + 31LL) / 32 * 4;
     const bool small = bitmap <= 40 * 1024;

@@ -1,16 +1,25 @@
 // gated_scan.cuh -- forward and backward of the gated linear recurrence over whole sequences.
 //
-// A row (b, d) is walked in tiles: lane k of SEG lanes holds 8 or 16 consecutive steps.  The recurrence
-// is composed of pairs (P, H), h -> P h + H: each lane forms its steps' pair, rounds of shuffles give every lane the state before its first step, and the lane runs its steps again from
-// there.  The backward does the same from the last tile to the first; the states come from the
-// checkpoints, one before every group, so it has to scan in one direction only.
+// A row (b, d) is walked in tiles: each of its lanes holds 8 or 16 consecutive steps.  The recurrence is composed
+// of pairs (P, H), h -> P h + H: each lane forms its steps' pair, rounds of shuffles give every lane the state
+// before its first step, and the lane runs its steps again from there.  The backward does the same from the
+// last tile to the first; the states come from the checkpoints, one before every group of 8, so it has to
+// scan in one direction only, and dx, dr, di, dz and the parameters' sums leave the same pass.
 //
 // SEG = 32: a warp per row.  SEG = 0: p.seg lanes per row, 1 to 16: several short rows per warp, so that few
-// lanes idle.
+// lanes idle (16 x 5120 rows of 100 steps, forward and backward: 295 -> 141 us).
 // SPLIT: the warps of a block, or of a cluster of blocks, share one row: of p.split warps in all each takes
-// every p.split-th tile, and a barrier a round joins their pairs, which every warp writes into the
-// shared memory of all blocks of the cluster.  That is for few long rows, which could not fill the GPU's
-// warps otherwise.
+// every p.split-th tile, and a barrier a round joins their pairs, which every warp writes into the shared
+// memory of all blocks of the cluster.  That is for few long rows, which could not fill the GPU's warps
+// otherwise (64 rows of 32768 steps: 60 -> 33 us).
+//
+// What bounds it (bf16 with the gate, B200): the bytes, and close behind them the special-function unit (5
+// operations a step forward: two exponentials, a reciprocal root, a reciprocal, a tanh) and issue (about 30
+// instructions a step forward, 65 backward, packed fp32 pairs throughout).  32768 steps of 5120 channels: 308 us,
+// 83% of the copy rate; forward 2048 steps of 8 x 1536 channels 50 us (77%), backward 82 us (87%), with
+// resets 56 and 100; fp32 the pair at 84%.  What was slower: the forward's operands through the backward's
+// ring (334 us); warps that stay and take the next row's first tile under way (backward 106 us: registers);
+// reset flags a tile ahead (+6 us).
 #pragma once
 
 #include <type_traits>
@@ -27,18 +36,14 @@ __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
 }
 
 constexpr int kGatedWarps = 4;  // warps of a block without SPLIT
-constexpr int kMaxSplit = 8;   // warps of a block with SPLIT
-constexpr int kMaxParts = 32;  // warps that share a row
-constexpr int kMaxCluster = 8;
-#ifndef FWD_MINB
-#define FWD_MINB 4
-#endif
-#ifndef BWD_MINB32
-#define BWD_MINB32 3
-#endif
-#ifndef BWD_MINB
-#define BWD_MINB 4
-#endif
+constexpr int kMaxSplit = 8;    // warps of a block with SPLIT (two such blocks per SM)
+constexpr int kMaxParts = 32;   // warps that share a row
+constexpr int kMaxCluster = 8;  // blocks that share a row
+// Blocks per SM that the registers are held to, so 128 registers, or 168 for the fp32 backward (3: 56 us on
+// 3 x 1001 x 2047, 4: 63).  More blocks spill: 5 took 432 us against 313 (forward, 5120 x 32768), 147 against 111
+// (backward, 8 x 1536 x 2048).
+constexpr int kFwdBlocks = 4;
+template <typename IO> constexpr int kBwdBlocks = sizeof(IO) == 2 ? 4 : 3;
 
 // Dynamic shared memory of a block of the backward: the ring, and the checkpoints' slots.
 template <typename IO>
@@ -85,12 +90,12 @@ struct RowPlace {
     unsigned row;
     int seg, lane;    // lanes per row; 0 .. seg - 1
     int part, parts;  // which of the warps that share the row
-    unsigned blocks, rank;  // of the cluster that shares it
+    int blocks, rank; // of the cluster that shares the row
     __device__ RowPlace(const GatedParams& p) {
         seg = SEG ? SEG : p.seg;
         lane = threadIdx.x & (seg - 1);
         blocks = SPLIT ? p.blocks : 1;
-        rank = blocks > 1 ? cluster_rank() : 0;
+        rank = blocks > 1 ? static_cast<int>(cluster_rank()) : 0;
         part = SPLIT ? rank * (blockDim.x / 32) + threadIdx.x / 32 : 0;
         parts = SPLIT ? p.split : 1;
         row = SPLIT ? blockIdx.x / blocks : blockIdx.x * (kGatedWarps * 32 / seg) + threadIdx.x / seg;
@@ -109,6 +114,7 @@ __device__ __forceinline__ float join_parts(float2* pairs, int place, int parts,
     } else {
         const float2 v = make_float2(__shfl_sync(kAll, P, writer), __shfl_sync(kAll, H, writer));
         if (lane < blocks) st_cluster(pairs + place, lane, v);
+        __syncwarp();
         cluster_arrive();
         cluster_wait();
     }
@@ -122,7 +128,8 @@ __device__ __forceinline__ float join_parts(float2* pairs, int place, int parts,
 }
 
 template <typename IO, bool GATE, bool RESET, int SEG, bool SPLIT>
-__global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPLIT ? 2 : FWD_MINB) gated_fwd_kernel(const GatedParams p) {
+__global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPLIT ? 2 : kFwdBlocks)
+    gated_fwd_kernel(const GatedParams p) {
     constexpr int N = kFwdSteps<IO>, kPairs = N / 2, kIn = 3;
     __shared__ float2 pairs[SPLIT ? 2 : 1][SPLIT ? kMaxParts : 1];
     const RowPlace<SEG, SPLIT> at(p);
@@ -157,16 +164,14 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
                                                   static_cast<unsigned>(p.x.bs) % n, static_cast<unsigned>(p.x.ds) % n, 0};
     }
 
-    constexpr bool kAhead = sizeof(IO) == 2 || F32_AHEAD;
-    int t0 = (at.part * at.seg + at.lane) * N - phase;
+        int t0 = (at.part * at.seg + at.lane) * N - phase;
     const int stride = at.parts * at.seg * N;
     Raw<IO, N> next[kIn];
-    if (kAhead) load_steps(in, vec, all_vec, t0, valid ? p.L : 0, reach, next);  // (not waiting for len)
+    load_steps(in, vec, all_vec, t0, valid ? p.L : 0, reach, next);  // (not waiting for len)
     int round = 0;
 #pragma unroll 1
     for (int t = -phase; SEG == 32 ? t < len : __any_sync(kAll, t < len); t += stride, t0 += stride, ++round) {
         float2 a[kPairs], u[kPairs], v[kPairs], w[kPairs];
-        if (!kAhead) load_steps(in, vec, all_vec, t0, len, reach, next);
         const unsigned inside = steps_inside<N>(t0, len);
         if (inside != all_steps<N>) mask_steps<IO, N>(inside, next[0], 0), mask_steps<IO, N>(inside, next[1], shut<IO>), mask_steps<IO, N>(inside, next[2], 0);
         unpack<IO, N>(next[0], u);
@@ -174,7 +179,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         unpack<IO, N>(next[2], w);
         Raw<IO, N> zc[1];
         if (GATE) load_steps(zrow, vz, vz[0], t0, len, reach, zc);  // wanted last
-        if (kAhead) load_steps(in, vec, all_vec, t0 + stride, len, reach, next);  // under way while this tile is computed
+        load_steps(in, vec, all_vec, t0 + stride, len, reach, next);  // under way while this tile is computed
         const auto coefficients = [&](auto near_tag) {
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) {
@@ -253,7 +258,8 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
 }
 
 template <typename IO, bool GATE, bool RESET, int SEG, bool SPLIT>
-__global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPLIT ? 2 : (sizeof(IO) == 2 ? BWD_MINB : BWD_MINB32)) gated_bwd_kernel(const GatedParams p) {
+__global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPLIT ? 2 : kBwdBlocks<IO>)
+    gated_bwd_kernel(const GatedParams p) {
     constexpr int N = kBwdSteps, kPairs = N / 2, kIn = GATE ? 5 : 4, kOut = GATE ? 4 : 3;
     __shared__ float2 pairs[SPLIT ? 2 : 1][SPLIT ? kMaxParts : 1];
     __shared__ float2 part_sums[SPLIT ? kMaxParts : 1][2];
@@ -492,6 +498,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
                 __syncthreads();
             } else {
                 if (at.lane == 0) st_cluster(&part_sums[at.part][0], 0, make_float2(sT, sr)), st_cluster(&part_sums[at.part][1], 0, make_float2(si, 0.f));
+                __syncwarp();
                 cluster_arrive();
                 cluster_wait();
             }

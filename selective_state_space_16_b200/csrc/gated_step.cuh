@@ -8,10 +8,11 @@
 
 namespace ssm {
 
-#ifndef STEP_BLOCKS
-#define STEP_BLOCKS 6
-#endif
 constexpr int kStepThreads = 128;
+// Resident blocks per SM (80 registers), which is also how many a launch has at most.  bf16 with the gate, graph
+// of 60 steps: 256 x 5120 6.1 us and 2048 x 5120 36 us (75% of the copy rate), with 8 blocks 6.2 and 34 but
+// fp32 512 x 8192 19.1 instead of 18.8 (spills), with 10 9.1 and 65; one row per block 7.2 and 69.
+constexpr int kStepBlocks = 6;
 constexpr int kStepChannels = 4;  // per thread
 
 struct GatedStep {
@@ -79,7 +80,7 @@ __device__ __forceinline__ void store4(T* p, int d, int dim, bool vec, const flo
 // slots in a bitmap while its first loads are under way; only if so does it search the list row by row
 // (no_bitmap: more slots than shared memory has bits for, search at once).
 template <typename IO, bool GATE>
-__global__ void __launch_bounds__(kStepThreads, STEP_BLOCKS) gated_step_kernel(const GatedStep g) {
+__global__ void __launch_bounds__(kStepThreads, kStepBlocks) gated_step_kernel(const GatedStep g) {
     extern __shared__ unsigned seen[];
     const ssm_gated_step_t& p = g.a;
     const int d = (blockIdx.x * kStepThreads + threadIdx.x) * kStepChannels;
