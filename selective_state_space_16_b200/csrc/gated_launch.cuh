@@ -67,7 +67,7 @@ ssm_status_t launch_gated(ssm::GatedParams p, bool backward, int sms, cudaStream
                                   : (reset ? gated_kernel<IO, false, true>(shape, backward) : gated_kernel<IO, false, false>(shape, backward));
     const int block = shape.split > 1 ? shape.split / shape.blocks * 32 : ssm::kGatedWarps * 32;
     const long long per_block = block / shape.seg;
-    const int smem = backward ? ssm::bwd_smem<IO>(gate, block) : 0;
+    const int smem = backward ? ssm::bwd_smem<IO>(gate, reset, block) : 0;
     if (smem > 46 * 1024 &&  // (with the static part of it, past the 48 KB that need no asking)
         !ensure_smem_attr(reinterpret_cast<const void*>(kern), smem)) return SSM_ERR_LAUNCH;
     cudaLaunchConfig_t cfg{};

@@ -30,9 +30,12 @@ namespace ssm {
 
 constexpr unsigned kAll = 0xffffffffu;
 
-// 4-byte asynchronous copy global -> shared.
+// 4- and 8-byte asynchronous copies global -> shared.
 __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_8(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
 constexpr int kGatedWarps = 4;  // warps of a block without SPLIT
@@ -45,10 +48,10 @@ constexpr int kMaxCluster = 8;  // blocks that share a row
 constexpr int kFwdBlocks = 4;
 template <typename IO> constexpr int kBwdBlocks = sizeof(IO) == 2 ? 4 : 3;
 
-// Dynamic shared memory of a block of the backward: the ring, and the checkpoints' slots.
+// Dynamic shared memory of a block of the backward: the ring, and slots for the checkpoints and reset flags.
 template <typename IO>
-constexpr int bwd_smem(bool gate, int threads) {
-    return kBwdStages<IO> * ((gate ? Ring<IO, kBwdSteps, 5>::kVecs : Ring<IO, kBwdSteps, 4>::kVecs) * 16 + 4) * threads;
+constexpr int bwd_smem(bool gate, bool reset, int threads) {
+    return kBwdStages<IO> * ((gate ? Ring<IO, kBwdSteps, 5>::kVecs : Ring<IO, kBwdSteps, 4>::kVecs) * 16 + 4 + (reset ? 8 : 0)) * threads;
 }
 
 // The product of a lane's decays, as join.
@@ -303,10 +306,17 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     using In = Ring<IO, N, kIn>;
     constexpr int kStages = kBwdStages<IO>;
     extern __shared__ uint4 ring[];
-    float* states_in = reinterpret_cast<float*>(ring + kStages * In::kVecs * blockDim.x) + threadIdx.x;  // the checkpoints' slots
+    auto* flags_in = reinterpret_cast<unsigned long long*>(ring + kStages * In::kVecs * blockDim.x) + threadIdx.x;
+    float* states_in = reinterpret_cast<float*>(flags_in - threadIdx.x + (RESET ? kStages * blockDim.x : 0)) + threadIdx.x;
     const auto load = [&](int stage, int t) {
         const int t0 = t + (at.part * at.seg + at.lane) * N;
         const bool active = t >= -phase;
+        if (RESET) {
+            if (active && t0 >= 0 && t0 + 8 <= len && (reinterpret_cast<uintptr_t>(reset + t0) & 7) == 0)
+                cp_async_8(flags_in + stage * blockDim.x, reset + t0);
+            else
+                flags_in[stage * blockDim.x] = reset_flags(reset, t0, active ? len : -N, p.reset, reset_end);
+        }
         if (active && t0 < len) cp_async_4(states_in + stage * blockDim.x, ckpt + (t0 + phase) / kGroup);
         In::load(ring, stage, in, vin, all_vec, t0, active ? len : -N, reach);
     };
@@ -323,16 +333,19 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         const bool whole = inside == all_steps<N>;
         float2 a[kPairs], g[kPairs], kx[kPairs], ki[kPairs], kT[kPairs], kr[kPairs], b[kPairs], ax[kPairs];
         Raw<IO, N> raw[kIn];
+        unsigned long long flags = 0;
         float h = 0.f;
         if constexpr (kStages > 0) {
             cp_async_wait<kStages - 2>();
 #pragma unroll
             for (int k = 0; k < kIn; ++k) raw[k] = In::read(ring, stage, k);
             if (t0 < end && active) h = states_in[stage * blockDim.x];
+            if (RESET) flags = flags_in[stage * blockDim.x];
             load(stage == 0 ? kStages - 1 : stage - 1, t - (kStages - 1) * stride);
             stage = stage == kStages - 1 ? 0 : stage + 1;
         } else {
             if (t0 < end && active) h = ckpt[(t0 + phase) / kGroup];
+            if (RESET) flags = reset_flags(reset, t0, end, p.reset, reset_end);
             load_steps(in, vin, all_vec, t0, active ? end : -N, reach, raw);
         }
         if (!whole) {
@@ -343,12 +356,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         unpack<IO, N>(raw[1], kr);
         unpack<IO, N>(raw[2], ki);
         unpack<IO, N>(raw[3], g);
-        bool any_cut = false;
-        unsigned long long flags = 0;
-        if (RESET) {
-            flags = reset_flags(reset, t0, end, p.reset, reset_end);
-            any_cut = __any_sync(kAll, flags != 0);
-        }
+        const bool any_cut = RESET && __any_sync(kAll, flags != 0);
         // what g_t is to be multiplied by, for each gradient:
         //   dx  kx = m iota         di  ki = b (1 - iota), b = m iota x
         //   T = a (iota x a v / m - h_{t-1} v) = kT - h_{t-1} ax       dr  T kr, kr = 1 - rho
