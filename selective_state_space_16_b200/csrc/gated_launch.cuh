@@ -2,6 +2,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 
 #include "gated_host.h"
 #include "gated_scan.cuh"
@@ -16,13 +17,23 @@ struct GatedShape {
     int seg, split, blocks;
 };
 
-// Splitting goes on, by twos, until the GPU has 8 warps per SM (16 are resident) or a round covers the
-// row: up to 4 warps of one block, then with fewer rows than SMs up to 8 blocks, else up to 8 warps.
-// Forward and backward of bf16 rows with a gate, us: 64 x 32768 60 with 4 warps, 44 with 16 in a block, 33
-// with 4 x 8 blocks; 128 x 32768 61, 47 and 47 (4 x 4); 200 x 16384 45 with 4, 43 with 8, 43 with 4 x 2 blocks;
-// 300 x 16384 53 with 4, 57 with 8, 64 with 4 x 2; 768 x 16384 121, 92, 92 and 100 with 1, 2, 4 and 8; 1536 x 8192
-// 86 and 93 with 1 and 2.  3 or 6 warps took longer than 2 and 4 throughout.
-inline GatedShape split_shape(long long rows, int L, int steps, int sms) {
+// How full the waves of 16 warps per SM are, if each of `warps` is a warp's work.
+inline double wave_fill(long long warps, int sms) {
+    const double waves = static_cast<double>(warps) / (16. * sms);
+    return waves / std::ceil(waves);
+}
+
+// Splitting goes on, by twos, until the GPU has 8 warps per SM (16 are resident) or a round covers the row: up to
+// 4 warps of one block, then with fewer rows than SMs up to 8 blocks, else up to 8 warps.  Forward and backward of
+// bf16 rows with a gate, us: 64 x 32768 60 with 4 warps, 44 with 16 in a block, 33 with 4 x 8 blocks; 128 x 32768 61,
+// 47 and 47 (4 x 4); 200 x 16384 45 with 4, 43 with 8, 43 with 4 x 2 blocks; 300 x 16384 53 with 4, 57 with 8, 64 with
+// 4 x 2; 768 x 16384 121, 92, 92 and 100 with 1, 2, 4 and 8; 1536 x 8192 86 and 93 with 1 and 2.  3 or 6 warps took
+// longer than 2 and 4 throughout.
+// Long rows in a few waves are split too where that fills the last wave better: the barriers cost the forward about
+// 3%, the backward 8%.  Forward, us, with 1, 2 and 4 warps: 5120 x 32768 313, 292, 285; 5120 x 8192 92, 86, 90;
+// 3000 x 16384 118, 98, 96; 12288 x 8192 188, 182, 193; backward 2600 x 8192 100, 86, 90, 3000 x 16384 188, 180, 176,
+// 5120 x 8192 146, 152, 158.  Rows of 4 tiles lose: 12288 x 2048 64, 76 and 94.
+inline GatedShape split_shape(long long rows, int L, int steps, int sms, bool backward) {
     const long long tiles = (L + 32LL * steps - 1) / (32 * steps);
     int warps = 1, blocks = 1;
     while (rows * warps * blocks < 8LL * sms && warps * blocks < tiles) {
@@ -33,17 +44,21 @@ inline GatedShape split_shape(long long rows, int L, int steps, int sms) {
         else
             break;
     }
+    if (rows > 16LL * sms)
+        while (warps < (backward ? 2 : 4) && tiles >= (backward ? 16 : 8) * warps * warps &&
+               wave_fill(rows * warps * 2, sms) > (backward ? 1.3 : 1.06) * wave_fill(rows * warps, sms))
+            warps *= 2;
     return {32, warps * blocks, blocks};
 }
 
 template <typename IO>
-GatedShape gated_shape(long long rows, int L, int steps, int sms) {
+GatedShape gated_shape(long long rows, int L, int steps, int sms, bool backward) {
     constexpr int kVec = 16 / sizeof(IO);
     const long long need = L % kVec ? L + static_cast<long long>(kVec) - 1 : L;  // (rows then start anywhere in a vector)
     int seg = 1;
     while (seg < 32 && static_cast<long long>(seg) * steps < need) seg *= 2;
     if (seg < 32) return {seg, 1, 1};
-    return split_shape(rows, L, steps, sms);
+    return split_shape(rows, L, steps, sms, backward);
 }
 
 using GatedKernel = void (*)(const ssm::GatedParams);
@@ -58,7 +73,7 @@ GatedKernel gated_kernel(GatedShape shape, bool backward) {
 template <typename IO>
 ssm_status_t launch_gated(ssm::GatedParams p, bool backward, int sms, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.batch) * p.dim;
-    const GatedShape shape = gated_shape<IO>(rows, p.L, backward ? ssm::kBwdSteps : ssm::kFwdSteps<IO>, sms);
+    const GatedShape shape = gated_shape<IO>(rows, p.L, backward ? ssm::kBwdSteps : ssm::kFwdSteps<IO>, sms, backward);
     p.seg = shape.seg;
     p.split = shape.split;
     p.blocks = shape.blocks;
