@@ -54,10 +54,10 @@ constexpr int kGroup = 8;  // steps between two checkpoints
 template <typename IO> constexpr int kFwdSteps = sizeof(IO) == 2 ? 16 : 8;
 constexpr int kBwdSteps = 8;
 
-// Stages of the backward's ring (Ring); 0: none, operands loaded where they are used.  Forward and backward of
-// 8 x 1536 x 2048 bf16 steps: 166 us with 3 or 2 stages, 168 with 4, 182 without; fp32 backward of 3 x 1001 x 2047:
-// 56 us without, 70 with 2 (its operands take twice the room, and fewer warps are resident).
-template <typename IO> constexpr int kBwdStages = sizeof(IO) == 2 ? 3 : 0;
+// Stages of the backward's ring.  Forward and backward, us: 8 x 1536 x 2048 bf16 166 with 2 or 3, 168 with 4, 182
+// without a ring; fp32 254 without, 246 with 2, 244 with 3, but 64 x 32768 fp32 47, 43 and 55 (shared memory for fewer
+// blocks).
+template <typename IO> constexpr int kBwdStages = sizeof(IO) == 2 ? 3 : 2;
 
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
@@ -287,25 +287,31 @@ __device__ __forceinline__ void load_steps(const IO* const (&in)[IN], const bool
     }
 }
 
-// The same a few tiles ahead: every thread copies its own steps of the tiles to come into its own slots
-// of shared memory and reads them from there when their turn comes.  No other thread touches them,
-// so there is nothing to wait for but the thread's own copies; and the tiles under way take no
-// registers.
-template <typename IO, int N, int IN>
+// The same a few tiles ahead: the threads of a warp copy the steps of the tiles to come into slots of shared memory
+// and read them from there when their turn comes.  Nothing outside the warp touches its slots, so there is
+// nothing to wait for but its own copies; and the tiles under way take no registers.  A thread's slots lie
+// next to each other, in pairs exchanged so that reading them has no bank conflicts; a warp whose tile is whole
+// copies it in 512-byte pieces (COOP: a tile is one stretch of a row).
+template <typename IO, int N, int IN, bool COOP>
 struct Ring {
-    static constexpr int kV = Raw<IO, N>::kVecs, kVecs = IN * kV;  // 16-byte slots of an operand, of a stage
-    __device__ static uint4* slot(uint4* ring, int stage, int k) { return ring + (stage * kVecs + k) * blockDim.x + threadIdx.x; }
-
-    __device__ static void copy(uint4* ring, int stage, int k, const IO* row, int t0) {
-        const uint4* q = reinterpret_cast<const uint4*>(row + t0);
-#pragma unroll
-        for (int j = 0; j < kV; ++j) cp_async_16(slot(ring, stage, k * kV + j), q + j, 16);
+    static constexpr int kV = Raw<IO, N>::kVecs, kVecs = IN * kV;  // 16-byte slots of a thread for an operand, a stage
+    __device__ static uint4* slot(uint4* ring, int stage, int k, int chunk) {  // chunk of the warp's 32 * kV
+        if (kV == 2) chunk ^= chunk >> 3 & 1;
+        return ring + (stage * kVecs + k * kV) * blockDim.x + (threadIdx.x & ~31u) * kV + chunk;
     }
-    // One group of copies.
+    // One group of copies: steps [t0, t0 + N) of each thread.
     __device__ static void load(uint4* ring, int stage, const IO* const (&in)[IN], const bool (&vec)[IN], bool all_vec, int t0, int len,
                                 Reach reach) {
-        const bool whole = t0 >= reach.low && t0 + N <= reach.high;
-        if (all_vec && whole && t0 < len && t0 + N > 0) {
+        const int lane = threadIdx.x & 31;
+        const bool whole = t0 >= reach.low && t0 + N <= reach.high, all = all_vec && whole && t0 < len;
+        if (kV > 1 && COOP && __all_sync(0xffffffffu, all)) {
+            constexpr int kChunk = 16 / sizeof(IO);
+#pragma unroll
+            for (int k = 0; k < IN; ++k)
+#pragma unroll
+                for (int j = 0; j < kV; ++j)
+                    cp_async_16(slot(ring, stage, k, j * 32 + lane), in[k] + (t0 - lane * N) + (j * 32 + lane) * kChunk, 16);
+        } else if (all) {
 #pragma unroll
             for (int k = 0; k < IN; ++k) copy(ring, stage, k, in[k], t0);
         } else if (t0 < len && t0 + N > 0) {
@@ -317,16 +323,29 @@ struct Ring {
                     Raw<IO, N> g;
                     load_elements(in[k], t0, len, g);
 #pragma unroll
-                    for (int j = 0; j < kV; ++j) *slot(ring, stage, k * kV + j) = g.v[j];
+                    for (int j = 0; j < kV; ++j) *slot(ring, stage, k, lane * kV + j) = g.v[j];
                 }
             }
         }
         cp_async_commit();
     }
+    __device__ static void copy(uint4* ring, int stage, int k, const IO* row, int t0) {
+        const uint4* q = reinterpret_cast<const uint4*>(row + t0);
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) cp_async_16(slot(ring, stage, k, lane * kV + j), q + j, 16);
+    }
+    // After it the oldest of STAGES - 1 groups has arrived.
+    template <int STAGES>
+    __device__ static void wait() {
+        cp_async_wait<STAGES - 2>();
+        if (kV > 1 && COOP) __syncwarp();
+    }
     __device__ static Raw<IO, N> read(uint4* ring, int stage, int k) {
         Raw<IO, N> s;
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int j = 0; j < kV; ++j) s.v[j] = *slot(ring, stage, k * kV + j);
+        for (int j = 0; j < kV; ++j) s.v[j] = *slot(ring, stage, k, lane * kV + j);
         return s;
     }
 };

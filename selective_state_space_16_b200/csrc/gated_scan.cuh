@@ -42,16 +42,16 @@ constexpr int kGatedWarps = 4;  // warps of a block without SPLIT
 constexpr int kMaxSplit = 8;    // warps of a block with SPLIT (two such blocks per SM)
 constexpr int kMaxParts = 32;   // warps that share a row
 constexpr int kMaxCluster = 8;  // blocks that share a row
-// Blocks per SM that the registers are held to, so 128 registers, or 168 for the fp32 backward (3: 56 us on
-// 3 x 1001 x 2047, 4: 63).  More blocks spill: 5 took 432 us against 313 (forward, 5120 x 32768), 147 against 111
-// (backward, 8 x 1536 x 2048).
+// Blocks per SM that the registers are held to, so 128 registers, or 168 for the fp32 backward (3 x 1001 x 2047
+// forward and backward: 77 us with 3, 81 with 4).  More blocks spill: 5 took 432 us against 313 (forward, 5120 x
+// 32768), 147 against 111 (backward, 8 x 1536 x 2048).
 constexpr int kFwdBlocks = 4;
 template <typename IO> constexpr int kBwdBlocks = sizeof(IO) == 2 ? 4 : 3;
 
 // Dynamic shared memory of a block of the backward: the ring, and slots for the checkpoints and reset flags.
 template <typename IO>
 constexpr int bwd_smem(bool gate, bool reset, int threads) {
-    return kBwdStages<IO> * ((gate ? Ring<IO, kBwdSteps, 5>::kVecs : Ring<IO, kBwdSteps, 4>::kVecs) * 16 + 4 + (reset ? 8 : 0)) * threads;
+    return kBwdStages<IO> * ((gate ? Ring<IO, kBwdSteps, 5, true>::kVecs : Ring<IO, kBwdSteps, 4, true>::kVecs) * 16 + 4 + (reset ? 8 : 0)) * threads;
 }
 
 // The product of a lane's decays, as join.
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
 #pragma unroll
         for (int k = 0; k < kOut; ++k) store_steps(out[k], t0, steps_inside<N>(t0, L), vout[k], zero);
     }
-    using In = Ring<IO, N, kIn>;
+    using In = Ring<IO, N, kIn, SEG == 32>;
     constexpr int kStages = kBwdStages<IO>;
     extern __shared__ uint4 ring[];
     auto* flags_in = reinterpret_cast<unsigned long long*>(ring + kStages * In::kVecs * blockDim.x) + threadIdx.x;
@@ -335,19 +335,13 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         Raw<IO, N> raw[kIn];
         unsigned long long flags = 0;
         float h = 0.f;
-        if constexpr (kStages > 0) {
-            cp_async_wait<kStages - 2>();
+        In::template wait<kStages>();
 #pragma unroll
-            for (int k = 0; k < kIn; ++k) raw[k] = In::read(ring, stage, k);
-            if (t0 < end && active) h = states_in[stage * blockDim.x];
-            if (RESET) flags = flags_in[stage * blockDim.x];
-            load(stage == 0 ? kStages - 1 : stage - 1, t - (kStages - 1) * stride);
-            stage = stage == kStages - 1 ? 0 : stage + 1;
-        } else {
-            if (t0 < end && active) h = ckpt[(t0 + phase) / kGroup];
-            if (RESET) flags = reset_flags(reset, t0, end, p.reset, reset_end);
-            load_steps(in, vin, all_vec, t0, active ? end : -N, reach, raw);
-        }
+        for (int k = 0; k < kIn; ++k) raw[k] = In::read(ring, stage, k);
+        if (t0 < end && active) h = states_in[stage * blockDim.x];
+        if (RESET) flags = flags_in[stage * blockDim.x];
+        load(stage == 0 ? kStages - 1 : stage - 1, t - (kStages - 1) * stride);  // into the slots read a tile ago
+        stage = stage == kStages - 1 ? 0 : stage + 1;
         if (!whole) {
 #pragma unroll
             for (int k = 0; k < kIn; ++k) mask_steps<IO, N>(inside, raw[k], k == 1 ? shut<IO> : 0);
