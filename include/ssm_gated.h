@@ -17,7 +17,9 @@
  *   - x, r, i, z, y and their gradients have io_dtype elements (fp32 or bf16), shape (batch, dim,
  *     seqlen) with consecutive steps next to each other; the batch and channel strides are given
  *     (in elements), so that slices of a wider tensor, such as the three parts of one
- *     projection's output, are taken as they are.  Any alignment of the elements' own size.
+ *     projection's output, are taken as they are.  Any alignment of the elements' own size.  What lies
+ *     between an operand's first and last row has to be readable memory: a few elements beside a row may
+ *     be read with it (and are never used).
  *   - lam, r_bias, i_bias, their gradients and every state are fp32 and dense; arithmetic is fp32.
  *   - lengths  NULL, or int32 (batch) on the device: row b has lengths[b] steps (values outside
  *     0 .. seqlen are taken as the nearest of the two).  What lies behind them is not read for any
@@ -129,7 +131,8 @@ typedef struct {
 /*
  * One step of the recurrence for every batch row, on the states of a pool.  A row whose slot is
  * outside 0 .. n_slots-1 pads the batch: it is skipped and its row of y left as it was.  Rows that
- * name the same slot are its consecutive tokens: they are applied in batch order.
+ * name the same slot are its consecutive tokens: they are applied in batch order.  y may not overlap
+ * the inputs.
  */
 ssm_status_t ssm_gated_state_update(const ssm_gated_step_t* args, ssm_stream_t stream);
 

@@ -82,7 +82,7 @@ __device__ __forceinline__ float softplus_lam(float lam) {
     constexpr float c[] = SSM_LOG1P_POLY;
     constexpr float kLog2eLow = 1.925963e-8f;  // log2(e) - kLog2e
     const float x = -fabsf(lam), y = x * kLog2e;
-    const float low = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -y));
+    const float low = x > -1e3f ? fmaf(x, kLog2eLow, fmaf(x, kLog2e, -y)) : 0.f;  // (-inf: 0, not NaN)
     float e = ex2_mufu(y);
     e = fmaf(e, low * kLn2, e);
     float p = c[8];

@@ -217,12 +217,24 @@ def ssm_gated_scan_bwd(x, r, i, lam, r_bias, i_bias, z, dy, dx, dr, di, dlam, dr
 def ssm_gated_state_update(state, x, r, i, lam, r_bias, i_bias, z, y, slots=None, c=8.0, stream=None, check=True):
     """Marshal a one-token step.  state: (slots, d) fp32 in/out, rows of any stride; x/r/i/z/y: (b, d), rows of
     any stride; slots: (b) int32, the state of each row (outside the pool: the row is skipped), or None."""
+    # (the checks are written out here: this call's host time is most of a small step)
     io, dtype, shape, dev = _io(x, 2)
     b, d = shape
-    like = (x, dtype, shape, dev)
-    at = (x.data_ptr(), _like(r, "r", *like), _like(i, "i", *like), 0 if z is None else _like(z, "z", *like), _like(y, "y", *like))
-    strides = (x.stride(), r.stride(), i.stride(), (0, 1) if z is None else z.stride(), y.stride())
-    (xs, xc), (rs, rc), (is_, ic), (zs, zc), (ys, yc) = strides
+    xs, xc = x.stride()
+    if r.dtype is not dtype or r.shape != shape or r.get_device() != dev:
+        _like(r, "r", x, dtype, shape, dev)
+    rs, rc = r.stride()
+    if i.dtype is not dtype or i.shape != shape or i.get_device() != dev:
+        _like(i, "i", x, dtype, shape, dev)
+    is_, ic = i.stride()
+    if y.dtype is not dtype or y.shape != shape or y.get_device() != dev:
+        _like(y, "y", x, dtype, shape, dev)
+    ys, yc = y.stride()
+    zp = zs = 0
+    zc = 1
+    if z is not None:
+        zp = _like(z, "z", x, dtype, shape, dev)
+        zs, zc = z.stride()
     if state.dtype is not torch.float32 or state.dim() != 2 or state.shape[1] != d or state.get_device() != dev:
         raise ValueError(f"state: expected (slots, {d}) torch.float32 on cuda:{dev}")
     ss, sc = state.stride()
@@ -231,9 +243,9 @@ def ssm_gated_state_update(state, x, r, i, lam, r_bias, i_bias, z, y, slots=None
     if lam is None:
         raise ValueError("lam is required")
     ch = (d,)
-    args = _STEP.pack(state.data_ptr(), ss, _dense(slots, "slots", (b,), _I32, dev), *at, xs, rs, is_, zs, ys,
-                      _dense(lam, "lam", ch, _F32, dev), _dense(r_bias, "r_bias", ch, _F32, dev),
-                      _dense(i_bias, "i_bias", ch, _F32, dev), b, d, state.shape[0], io, c)
+    args = _STEP.pack(state.data_ptr(), ss, _dense(slots, "slots", (b,), _I32, dev), x.data_ptr(), r.data_ptr(), i.data_ptr(), zp,
+                      y.data_ptr(), xs, rs, is_, zs, ys, _dense(lam, "lam", ch, _F32, dev),
+                      _dense(r_bias, "r_bias", ch, _F32, dev), _dense(i_bias, "i_bias", ch, _F32, dev), b, d, state.shape[0], io, c)
     code = _call(dev, stream, _lib().ssm_gated_state_update, args)
     if check:
         _check(code, "ssm_gated_state_update")

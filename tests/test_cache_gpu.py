@@ -177,6 +177,27 @@ def test_compact_many(cuda_device):
     assert same(pools, want) and du.tolist() == used1 and dt.tolist() == table1
 
 
+def test_empty(cuda_device):
+    """No slots, no layers, empty pages, empty lists."""
+    none = ssm.CachePools([torch.empty(3, 0, 5, device="cuda")])
+    used, kids, count = torch.empty(0, dtype=torch.int32, device="cuda"), i32(7, 7), i32(7)
+    ws = ssm.new_cache_workspace(none, 2)
+    ssm.ssm_cache_fork(none, used, i32(-1, 0), kids, ws)
+    table = i32(0, 3)
+    ssm.ssm_cache_compact(none, used, table, None, count, ws)
+    ssm.ssm_cache_copy(none, i32(0), i32(1), ws)
+    ssm.ssm_cache_free(none, used, i32(0, 2), zero_pages=True)
+    assert kids.tolist() == [-1, -1] and count.tolist() == [0] and table.tolist() == [-1, -1]
+    thin = [torch.empty(0, 6, 4, device="cuda"), torch.empty(2, 6, 0, device="cuda")]  # only the bookkeeping is left
+    h = ssm.CachePools(thin)
+    used, kids = i32(1, 0, 0, 1, 0, 1), i32(7, 7)
+    ws = ssm.new_cache_workspace(h, 2)
+    ssm.ssm_cache_fork(h, used, i32(3, -1), kids, ws)
+    ssm.ssm_cache_free(h, used, i32(0))
+    ssm.ssm_cache_compact(h, used, kids, None, None, ws)
+    assert used.tolist() == [1, 1, 1, 1, 0, 0] and kids.tolist() == [1, 2]
+
+
 def test_far_offsets(cuda_device):
     """A pool of more than 2^32 bytes: slots and layers beyond 32-bit offsets."""
     pool = torch.empty(2, 3, (1 << 30) + 16, dtype=torch.uint8, device="cuda")

@@ -129,6 +129,50 @@ def test_saturated_gates(cuda_device, io):
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_shut_gates_leave_the_state_alone(cuda_device, io):
+    """A recurrence gate of the type's lowest value or -inf (a masked step) keeps the state, and its step has no
+    gradient; an input gate so shut lets nothing in; lam = -inf freezes a channel.  From group to group of 8 steps
+    the state is composed anew, of at most 6 products and sums of magnitudes up to the largest state: it may move
+    by 12 half steps of that, and is the same bit for bit inside a group."""
+    t, dy, dlast = inputs(2, 4, 90, io, gate=False, seed=43)
+    low = torch.finfo(IO[io]).min
+    t["r"][0, :, 20:60], t["r"][1, :, 20:60] = low, float("-inf")
+    t["x"][:, :, 30:40] = 1e30
+    t["i"][0, :, 70:], t["i"][1, :, 70:] = low, float("-inf")
+    t["lam"][0] = float("-inf")
+    got = run_all(t, dy, dlast, True)
+    y = got["y"].float()
+    for a in range(24, 56, 8):
+        assert torch.equal(y[:, :, a:a + 8], y[:, :, a:a + 1].expand(-1, -1, 8))
+    most = y.abs().amax(2, keepdim=True) + t["initial_state"].abs()[..., None]
+    moved = (y[:, :, 20:60] - y[:, :, 19:20]).abs()
+    assert bool((moved <= (12 * U / 2 * most if io == "f32" else 2.0 ** -7 * y[:, :, 19:20].abs())).all())
+    for k in ("dx", "dr", "di"):
+        assert not bool(got[k][:, :, 20:60].any()), k
+    assert not bool(got["dx"][:, :, 70:].any()) and not bool(got["di"][:, :, 70:].any())
+    assert torch.equal(got["last"][:, 0], t["initial_state"][:, 0])
+    assert all(bool(torch.isfinite(got[k]).all()) for k in GRADS if got[k] is not None)
+
+
+@pytest.mark.parametrize("io,D,L", [("f32", 2600, 4100), ("bf16", 3000, 8192)])
+def test_many_long_rows(cuda_device, io, D, L):
+    """Shapes whose last wave is filled by splitting rows: every 97th channel against the reference."""
+    g = torch.Generator("cuda").manual_seed(47)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    t = {k: rnd(1, D, L).to(IO[io]) for k in ("x", "r", "i", "z")}
+    t.update(lam=torch.linspace(-9, 2, D, device="cuda"), r_bias=0.3 * rnd(D), i_bias=0.3 * rnd(D), initial_state=rnd(1, D),
+             lengths=torch.tensor([L - 5], dtype=torch.int32, device="cuda"), reset=None)
+    dy, dlast = rnd(1, D, L).to(IO[io]), rnd(1, D)
+    got = run_all(t, dy, dlast, True)
+    pick = slice(3, None, 97)
+    some = {k: v if v is None or k == "lengths" else v[pick] if v.dim() == 1 else v[:, pick] for k, v in t.items()}
+    want = reference(**some, dy=dy[:, pick], dlast=dlast[:, pick], bf16=io == "bf16")
+    for k, w in want.items():
+        check(got[k][pick] if got[k].dim() == 1 else got[k][:, pick], w, f"{io} {k}")
+    assert all(bool(torch.isfinite(got[k]).all()) for k in GRADS)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("B,D,L", [(1, 1, 40000), (1, 3, 9001), (2, 700, 129), (1, 2500, 77), (40, 130, 60), (2, 75, 2500), (1, 170, 5003),
                                    (1, 90, 4100), (4, 150, 1030)])
 def test_shapes(cuda_device, io, B, D, L):
@@ -193,6 +237,45 @@ def test_transposed_batch_and_channels(cuda_device):
     for k in ("x", "r", "i", "z"):
         t[k] = t[k].transpose(0, 1).contiguous().transpose(0, 1)
     compare(run_all(t, dy, dlast, True), t, dy, dlast, "transposed")
+
+
+def test_broadcast_inputs(cuda_device):
+    """Operands shared by the batch rows or by the channels (stride 0); flags as bool."""
+    t, dy, dlast = inputs(3, 6, 333, "bf16", reset=0.02, seed=67)
+    t["r"], t["i"], t["z"] = t["r"][:1].expand(3, 6, 333), t["i"][:, :1].expand(3, 6, 333), t["z"][:1, :1].expand(3, 6, 333)
+    t["reset"] = t["reset"].bool()
+    dy = dy[:1].expand(3, 6, 333)
+    compare(run_all(t, dy, dlast, True), t, dy, dlast, "broadcast")
+
+
+def test_far_offsets(cuda_device):
+    """Rows and slots more than 2^32 bytes apart."""
+    far, L = (1 << 31) + 16, 100
+    buf = torch.empty(far + 12000, dtype=torch.bfloat16, device="cuda")
+    at = lambda k, v=None: (lambda w: w if v is None else w.copy_(v))(buf.as_strided((2, 3, L), (far, 128, 1), 1000 * k))  # noqa: E731
+    t, dy, dlast = inputs(2, 3, L, "bf16", seed=71)
+    for k, name in enumerate(("x", "r", "i", "z")):
+        t[name] = at(k, t[name])
+    dy = at(4, dy)
+    out = {k: at(5 + n) for n, k in enumerate(("y", "dx", "dr", "di", "dz"))}
+    last, dh0, ck, ws = torch.empty(2, 3, device="cuda"), torch.empty(2, 3, device="cuda"), ssm.new_gated_checkpoints(2, 3, L), ssm.new_gated_workspace(2, 3, L)
+    dlam, drb, dib = (torch.empty(3, device="cuda") for _ in range(3))
+    a = [t[k] for k in ("x", "r", "i", "lam", "r_bias", "i_bias", "z")]
+    ssm.ssm_gated_scan_fwd(*a, out["y"], last, initial_state=t["initial_state"], checkpoints=ck)
+    ssm.ssm_gated_scan_bwd(*a, dy, out["dx"], out["dr"], out["di"], dlam, drb, dib, out["dz"], ws, initial_state=t["initial_state"],
+                           dlast_state=dlast, dinitial_state=dh0, checkpoints=ck)
+    compare(dict(out, last=last, dinitial_state=dh0, dlam=dlam, dr_bias=drb, di_bias=dib), t, dy, dlast, "far")
+    state = buf.view(torch.float32).as_strided((2, 3), (far // 2, 1), 5500)
+    state.copy_(torch.randn(2, 3))
+    y0, ey, st, est = step_reference(t, state, [1, 0], 0, True)
+    cols = [v[..., 0].contiguous() for v in (t["x"], t["r"], t["i"], t["z"])]
+    y = torch.empty(2, 3, dtype=torch.bfloat16, device="cuda")
+    ssm.ssm_gated_state_update(state, *cols[:3], t["lam"], t["r_bias"], t["i_bias"], cols[3], y,
+                               slots=torch.tensor([1, 0], dtype=torch.int32, device="cuda"))
+    check(y, (y0, ey), "far y")
+    check(state, (st, est), "far state")
+    del buf, t, a, out, dy, state
+    torch.cuda.empty_cache()
 
 
 def test_wanted_gradients_only(cuda_device):
@@ -284,6 +367,21 @@ def test_step(cuda_device, io, B, D, slots, gate):
         check(state, (st, est), f"step {k} state")
 
 
+def test_step_of_more_slots_than_a_bitmap_holds(cuda_device):
+    n, D, at = 400_000, 8, [399_999, 5, 399_999, -1, 400_000, 5, 7]
+    t, _, _ = inputs(7, D, 1, "f32", seed=53)
+    state = torch.randn(n, D, device="cuda")
+    y0, ey, st, est = step_reference(t, state, at, 0, False)
+    y = torch.full((7, D), 5.0, device="cuda")
+    cols = [t[v][..., 0].contiguous() for v in ("x", "r", "i", "z")]
+    ssm.ssm_gated_state_update(state, *cols[:3], t["lam"], t["r_bias"], t["i_bias"], cols[3], y,
+                               slots=torch.tensor(at, dtype=torch.int32, device="cuda"))
+    rows = [0, 1, 2, 5, 6]
+    check(y[rows], (y0[rows], ey[rows]), "many slots y")
+    check(state, (st, est), "many slots state")
+    assert bool((y[[3, 4]] == 5).all())
+
+
 def test_step_strided_rows(cuda_device):
     """Rows sliced from wider tensors, at odd offsets; the slots of a pool that holds more per slot."""
     for io in IO.values():
@@ -356,6 +454,22 @@ def test_captured_and_replayed_on_another_stream(cuda_device):
     side.synchronize()
     assert all(torch.equal(got[n], eager[n]) for n in ("y", "last"))
     assert all(torch.equal(got[n], eager[n]) for n in ("dx", "dr", "di", "dz"))
+
+
+def test_two_streams_at_once(cuda_device):
+    """Calls that overlap, each with its own buffers, give what they give alone."""
+    jobs = [inputs(2, 300, 1500, "bf16", seed=s) for s in (59, 61)]
+    alone = [run_all(t, dy, dlast, True) for t, dy, dlast in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [None, None]
+    for _ in range(3):
+        for k, ((t, dy, dlast), stream) in enumerate(zip(jobs, streams)):
+            with torch.cuda.stream(stream):
+                got[k] = run_all(t, dy, dlast, True)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, got):
+        assert all(torch.equal(a[n], b[n]) for n in a)
 
 
 def test_refusals(cuda_device):
