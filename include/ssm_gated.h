@@ -80,7 +80,7 @@ size_t ssm_gated_checkpoint_size(int batch, int dim, int64_t seqlen);
  * Forward scan.  y is required; last_state (batch, dim) and checkpoints (16-byte aligned, at least
  * ssm_gated_checkpoint_size() bytes) may be NULL.
  */
-ssm_status_t ssm_gated_scan_fwd(const ssm_gated_args_t* args, ssm_gated_out_t y, float* last_state, void* checkpoints,
+ssm_status_t ssm_gated_scan_fwd(const ssm_gated_args_t* args, const ssm_gated_out_t* y, float* last_state, void* checkpoints,
                                 ssm_stream_t stream);
 
 /* The gradients of a loss L for the backward.  Zero-initialise the whole struct. */

@@ -115,11 +115,13 @@ size_t ssm_gated_checkpoint_size(int batch, int dim, int64_t seqlen) {
     return sizeof(ssm::CkptHeader) + static_cast<size_t>(batch) * dim * checkpoint_row(seqlen) * sizeof(float);
 }
 
-ssm_status_t ssm_gated_scan_fwd(const ssm_gated_args_t* args, ssm_gated_out_t y, float* last_state, void* checkpoints,
+ssm_status_t ssm_gated_scan_fwd(const ssm_gated_args_t* args, const ssm_gated_out_t* out, float* last_state, void* checkpoints,
                                 ssm_stream_t stream) {
     GatedParams p;
     ssm_status_t st = common_params(args, &p);
     if (st != SSM_OK) return st;
+    if (!out) return SSM_ERR_INVALID_ARG;
+    const ssm_gated_out_t& y = *out;
     const bool rows = p.batch > 0 && p.dim > 0;
     if (rows && p.L > 0 && !y.data) return SSM_ERR_INVALID_ARG;
     if (is_input(args, y.data) || !element_aligned(y.data, args->io_dtype)) return SSM_ERR_INVALID_ARG;

@@ -19,11 +19,7 @@ from .binding import SSM_BF16, SSM_F32, _check
 _ARGS = struct.Struct("@Pqq Pqq Pqq Pqq PPP PPP q iiif")
 _GRADS = struct.Struct("@Pqq P Pqq Pqq Pqq Pqq PPPP")
 _STEP = struct.Struct("@Pq P PPPP P qqqqq PPP iiiif 4x")
-
-
-class GatedOut(ctypes.Structure):
-    """ssm_gated_out_t: a (batch, dim, seqlen) output."""
-    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("dim_stride", ctypes.c_int64)]
+_OUT = struct.Struct("@Pqq")
 
 
 def declare(lib: ctypes.CDLL) -> None:
@@ -33,7 +29,7 @@ def declare(lib: ctypes.CDLL) -> None:
     lib.ssm_gated_checkpoint_size.restype = sz
     lib.ssm_gated_bwd_workspace_size.argtypes = [ci, ci, i64, ci]
     lib.ssm_gated_bwd_workspace_size.restype = sz
-    lib.ssm_gated_scan_fwd.argtypes = [st, GatedOut, vp, vp, vp]
+    lib.ssm_gated_scan_fwd.argtypes = [st, st, vp, vp, vp]
     lib.ssm_gated_scan_fwd.restype = ci
     lib.ssm_gated_scan_bwd.argtypes = [st, st, vp, vp, sz, vp]
     lib.ssm_gated_scan_bwd.restype = ci
@@ -139,10 +135,21 @@ def _args(like, r, i, lam, r_bias, i_bias, z, initial_state, lengths, reset, c):
     x, dtype, shape, dev, io = like
     if lam is None:
         raise ValueError("lam is required")
+    # (written out rather than through _seq: a small call's host time is mostly this)
+    if r.dtype is not dtype or r.shape != shape or r.get_device() != dev:
+        _like(r, "r", x, dtype, shape, dev)
+    if i.dtype is not dtype or i.shape != shape or i.get_device() != dev:
+        _like(i, "i", x, dtype, shape, dev)
+    xb, xd, xl = x.stride()
+    rb, rd, rl = r.stride()
+    ib, id_, il = i.stride()
     b, d, L = shape
+    if not xl == rl == il == 1 and L > 1:
+        raise ValueError("x, r, i: consecutive steps must be next to each other (stride 1)")
+    zp, zb, zd = _seq(z, "z", x, dtype, shape, dev)
     ch = (d,)
-    return _ARGS.pack(*_seq(x, "x", x, dtype, shape, dev), *_seq(r, "r", x, dtype, shape, dev), *_seq(i, "i", x, dtype, shape, dev),
-                      *_seq(z, "z", x, dtype, shape, dev), _dense(lam, "lam", ch, _F32, dev), _dense(r_bias, "r_bias", ch, _F32, dev),
+    return _ARGS.pack(x.data_ptr(), xb, xd, r.data_ptr(), rb, rd, i.data_ptr(), ib, id_, zp, zb, zd,
+                      _dense(lam, "lam", ch, _F32, dev), _dense(r_bias, "r_bias", ch, _F32, dev),
                       _dense(i_bias, "i_bias", ch, _F32, dev), _dense(initial_state, "initial_state", (b, d), _F32, dev),
                       _dense(lengths, "lengths", (b,), _I32, dev), _dense(reset, "reset", (b, L), _FLAG, dev), L, b, d, io, c)
 
@@ -186,7 +193,7 @@ def ssm_gated_scan_fwd(x, r, i, lam, r_bias, i_bias, z, y, last_state, initial_s
     if y is None:
         raise ValueError("y is required")
     ck = 0 if checkpoints is None else _buffer(checkpoints, "checkpoints", ssm_gated_checkpoint_size(*shape), dev)
-    code = _call(dev, stream, _lib().ssm_gated_scan_fwd, args, GatedOut(*_seq(y, "y", x, dtype, shape, dev)),
+    code = _call(dev, stream, _lib().ssm_gated_scan_fwd, args, _OUT.pack(*_seq(y, "y", x, dtype, shape, dev)),
                  _dense(last_state, "last_state", shape[:2], _F32, dev), ck)
     if check:
         _check(code, "ssm_gated_scan_fwd")

@@ -1,7 +1,5 @@
 """The gated recurrence's C ABI without a device: sizes, refusals, struct layouts; and the 64-bit
 reference of the GPU tests against central differences."""
-import ctypes
-
 import numpy as np
 import pytest
 import torch
@@ -27,7 +25,7 @@ def args(x=P, r=P, i=P, z=0, lam=P, r_bias=0, i_bias=0, h0=0, lengths=0, reset=0
 
 
 def fwd(lib, y=2 * P, ys=(24, 8), last=None, ck=None, **kw):
-    return lib.ssm_gated_scan_fwd(args(**kw), gated.GatedOut(y, *ys), last, ck, None)
+    return lib.ssm_gated_scan_fwd(args(**kw), gated._OUT.pack(y, *ys), last, ck, None)
 
 
 def bwd(lib, dy=2 * P, dx=3 * P, dr=4 * P, di=5 * P, dz=0, dlam=0, ws=P, wsb=1 << 20, ds=(24, 8), ck=None, **kw):
@@ -44,7 +42,8 @@ def test_forward_refusals(lib):
         assert fwd(lib, **bad) == IV, bad
     assert fwd(lib, b=65536, d=32768) == UN
     assert fwd(lib, L=(1 << 31) - 1024) == UN
-    assert lib.ssm_gated_scan_fwd(None, gated.GatedOut(P, 24, 8), None, None, None) == IV
+    assert lib.ssm_gated_scan_fwd(None, gated._OUT.pack(P, 24, 8), None, None, None) == IV
+    assert lib.ssm_gated_scan_fwd(args(), None, None, None, None) == IV
     assert fwd(lib, b=0, x=0, r=0, i=0, y=0) == OK
     assert fwd(lib, d=0) == OK
 
@@ -93,7 +92,7 @@ def test_packed_structs_have_the_headers_layout(tmp_path):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     subprocess.check_call(["gcc", "-I", os.path.join(root, "include"), "-o", str(tmp_path / "s"), str(src)])
     got = [int(v) for v in subprocess.check_output([str(tmp_path / "s")]).split()]
-    assert got == [gated._ARGS.size, gated._GRADS.size, gated._STEP.size, ctypes.sizeof(gated.GatedOut), gated._ARGS.size - 4,
+    assert got == [gated._ARGS.size, gated._GRADS.size, gated._STEP.size, gated._OUT.size, gated._ARGS.size - 4,
                    gated._STEP.size - 8]
 
 
