@@ -88,6 +88,25 @@ ssm_status_t launch_move(const CacheMove& m, long long pairs, int sm_count, cuda
     return cudaLaunchKernelEx(&cfg, ssm::cache_move_kernel, m) == cudaSuccess ? launch_status() : SSM_ERR_LAUNCH;
 }
 
+bool is_small(const CacheMove& m, long long pairs, int n_list) {
+    return m.units * pairs <= ssm::kSmallUnits && m.n_slots <= ssm::kSmallSlots && n_list <= ssm::kSmallList;
+}
+
+template <ssm::CacheOp OP>
+ssm_status_t launch_small(const ssm::CacheSmall& c, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ssm::kSmallBlocks);
+    cfg.blockDim = dim3(ssm::kPlanThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute cluster{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = ssm::kSmallBlocks;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, ssm::cache_small_kernel<OP>, c) == cudaSuccess ? launch_status() : SSM_ERR_LAUNCH;
+}
+
 }  // namespace
 
 extern "C" {
@@ -111,15 +130,16 @@ ssm_status_t ssm_cache_copy(const ssm_cache_pool_t* pools, int n_pools, int n_sl
     st = check_device(&sms);
     if (st != SSM_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    m.n = n;
+    m.src = src;
+    m.dst = dst;
+    if (is_small(m, n, n)) return launch_small<ssm::CacheOp::kCopy>({m}, s);
     const int bitmap = (n_slots + 31) / 32 * 4;
     if (!ensure_smem_attr(reinterpret_cast<const void*>(ssm::cache_plan_copy_kernel), bitmap)) return SSM_ERR_LAUNCH;
     ssm::cache_plan_copy_kernel<<<1, ssm::kPlanThreads, bitmap, s>>>(src, dst, n, n_slots, w.plan);
     st = launch_status();
     if (st != SSM_OK) return st;
-    m.n = n;
     m.plan = w.plan;
-    m.src = src;
-    m.dst = dst;
     return launch_move(m, n, sms, s);
 }
 
@@ -139,14 +159,15 @@ ssm_status_t ssm_cache_fork(const ssm_cache_pool_t* pools, int n_pools, int n_sl
     st = check_device(&sms);
     if (st != SSM_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    ssm::cache_plan_fork_kernel<<<1, ssm::kPlanThreads, 0, s>>>(used, parents, children, n, n_slots, w.plan, w.src, w.dst);
-    st = launch_status();
-    if (st != SSM_OK) return st;
     m.n = n;
     m.may_clear = 1;
+    if (is_small(m, n, n)) return launch_small<ssm::CacheOp::kFork>({m, used, nullptr, nullptr, nullptr, parents, children, 0}, s);
+    ssm::cache_plan_fork_kernel<<<1, ssm::kPlanThreads, 0, s>>>(used, parents, children, n, n_slots, w.plan, w.src, w.dst, w.scratch);
+    st = launch_status();
+    if (st != SSM_OK) return st;
     m.plan = w.plan;
     m.src = w.src;
-    m.dst = children;
+    m.dst = w.dst;
     return launch_move(m, n, sms, s);
 }
 
@@ -187,6 +208,8 @@ ssm_status_t ssm_cache_compact(const ssm_cache_pool_t* pools, int n_pools, int n
     st = check_device(&sms);
     if (st != SSM_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (is_small(m, n_slots / 2, n_slots / 2))
+        return launch_small<ssm::CacheOp::kCompact>({m, used, table, remap, count, nullptr, nullptr, n_table}, s);
     ssm::cache_plan_compact_kernel<<<1, ssm::kPlanThreads, 0, s>>>(used, n_slots, table, n_table, remap, count, w.plan, w.src, w.dst,
                                                                    w.scratch);
     st = launch_status();

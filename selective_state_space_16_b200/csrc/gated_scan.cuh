@@ -24,6 +24,7 @@
 
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "gated_math.cuh"
 
 namespace ssm {
@@ -71,14 +72,6 @@ __device__ __forceinline__ float product(float2 (&a)[PAIRS]) {
         return q[0].x * q[0].y;
     }
 }
-
-__device__ __forceinline__ unsigned cluster_rank() {
-    unsigned r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Writes two floats to the same place of block `rank`'s shared memory as `here` in this one's.
 __device__ __forceinline__ void st_cluster(const float2* here, unsigned rank, float2 v) {

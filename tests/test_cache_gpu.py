@@ -198,6 +198,37 @@ def test_empty(cuda_device):
     assert used.tolist() == [1, 1, 1, 1, 0, 0] and kids.tolist() == [1, 2]
 
 
+@pytest.mark.parametrize("slots", [2048, 2049])
+def test_calls_on_either_side_of_the_small_ones(cuda_device, slots):
+    """The largest pool of a small call and the next one: every operation, on pages of odd sizes and strides."""
+    g = torch.Generator().manual_seed(slots)
+    wide = torch.randn(2, slots, 9, generator=g).cuda()
+    pools = [wide[:, :, 2:7], torch.randint(0, 256, (1, slots, 3), generator=g, dtype=torch.uint8).cuda(),
+             torch.randn(slots, 3, 4, generator=g).bfloat16().cuda().transpose(0, 1)]
+    keep = wide.clone()
+    h = ssm.CachePools(pools)
+    ws = ssm.new_cache_workspace(h, 40)
+    dense = lambda: [p.contiguous() for p in pools]  # noqa: E731
+    for pairs in ([(0, slots - 1), (slots - 2, 7), (5, 9)], [(0, 1), (1, slots - 1), (slots - 1, 2), (3, 2)]):
+        want = copied(dense(), pairs)
+        ssm.ssm_cache_copy(h, i32(*[p[0] for p in pairs]), i32(*[p[1] for p in pairs]), ws)
+        assert same(dense(), want)
+    used = (torch.rand(slots, generator=g) < 0.99).to(torch.int32)
+    parents = torch.randint(-1, slots, (30,), generator=g, dtype=torch.int32)
+    want, used1, kids = forked(dense(), used.tolist(), parents.tolist())
+    du, dc = used.cuda(), torch.empty(30, dtype=torch.int32, device="cuda")
+    ssm.ssm_cache_fork(h, du, parents.cuda(), dc, ws)
+    assert same(dense(), want) and dc.tolist() == kids and du.tolist() == used1
+    ended = torch.randperm(slots, generator=g)[:25].to(torch.int32)
+    ssm.ssm_cache_free(h, du, ended.cuda())
+    assert du.sum() == sum(used1) - sum(used1[e] for e in ended.tolist())
+    want, used2, table, remap, live = compacted(dense(), du.tolist(), list(range(slots)))
+    dt, dr, n = torch.arange(slots, dtype=torch.int32, device="cuda"), torch.empty(slots, dtype=torch.int32, device="cuda"), i32(0)
+    ssm.ssm_cache_compact(h, du, dt, dr, n, ws)
+    assert same(dense(), want) and du.tolist() == used2 and dt.tolist() == table and dr.tolist() == remap and n.tolist() == [live]
+    assert torch.equal(wide[:, :, :2], keep[:, :, :2]) and torch.equal(wide[:, :, 7:], keep[:, :, 7:])
+
+
 def test_far_offsets(cuda_device):
     """A pool of more than 2^32 bytes: slots and layers beyond 32-bit offsets."""
     pool = torch.empty(2, 3, (1 << 30) + 16, dtype=torch.uint8, device="cuda")
