@@ -77,11 +77,11 @@ typedef struct {
 size_t ssm_gated_checkpoint_size(int batch, int dim, int64_t seqlen);
 
 /*
- * Forward scan.  y is required; last_state (batch, dim) and checkpoints (16-byte aligned, at least
- * ssm_gated_checkpoint_size() bytes) may be NULL.
+ * Forward scan.  y is required; last_state (batch, dim) and checkpoints (16-byte aligned, of at least
+ * ssm_gated_checkpoint_size() bytes, else SSM_ERR_WORKSPACE) may be NULL.
  */
 ssm_status_t ssm_gated_scan_fwd(const ssm_gated_args_t* args, const ssm_gated_out_t* y, float* last_state, void* checkpoints,
-                                ssm_stream_t stream);
+                                size_t checkpoint_bytes, ssm_stream_t stream);
 
 /* The gradients of a loss L for the backward.  Zero-initialise the whole struct. */
 typedef struct {
@@ -113,7 +113,7 @@ size_t ssm_gated_bwd_workspace_size(int batch, int dim, int64_t seqlen, int have
  *                not initialised; not to be used by two calls that can overlap on the GPU.
  */
 ssm_status_t ssm_gated_scan_bwd(const ssm_gated_args_t* args, const ssm_gated_grads_t* grads, const void* checkpoints,
-                                void* workspace, size_t workspace_bytes, ssm_stream_t stream);
+                                size_t checkpoint_bytes, void* workspace, size_t workspace_bytes, ssm_stream_t stream);
 
 /* One-token step.  Zero-initialise the whole struct. */
 typedef struct {

@@ -77,7 +77,7 @@ def ssm_cache_copy(pools, src, dst, workspace, stream=None, check=True):
     if src.shape != dst.shape:
         raise ValueError(f"{src.numel()} sources, {dst.numel()} destinations")
     code = _call(pools.index, stream, _lib().ssm_cache_copy, pools.packed, pools.n_pools, pools.n_slots, a, b, src.numel(),
-                 _buffer(workspace, "workspace", 0, pools.index), workspace.nbytes)
+                 *_buffer(workspace, "workspace", pools.index))
     if check:
         _check(code, "ssm_cache_copy")
     return code
@@ -91,7 +91,7 @@ def ssm_cache_fork(pools, used, parents, children, workspace, stream=None, check
         raise ValueError(f"{parents.numel()} parents, {children.numel()} children")
     code = _call(pools.index, stream, _lib().ssm_cache_fork, pools.packed, pools.n_pools, pools.n_slots,
                  _dense(used, "used", (pools.n_slots,), _I32, pools.index), a, b, parents.numel(),
-                 _buffer(workspace, "workspace", 0, pools.index), workspace.nbytes)
+                 *_buffer(workspace, "workspace", pools.index))
     if check:
         _check(code, "ssm_cache_fork")
     return code
@@ -113,8 +113,7 @@ def ssm_cache_compact(pools, used, table, remap, count, workspace, stream=None, 
     code = _call(pools.index, stream, _lib().ssm_cache_compact, pools.packed, pools.n_pools, pools.n_slots,
                  _dense(used, "used", (pools.n_slots,), _I32, pools.index), 0 if table is None else _list(table, "table", pools),
                  0 if table is None else table.numel(), _dense(remap, "remap", (pools.n_slots,), _I32, pools.index),
-                 _dense(count, "count", (1,), _I32, pools.index), _buffer(workspace, "workspace", 0, pools.index),
-                 workspace.nbytes)
+                 _dense(count, "count", (1,), _I32, pools.index), *_buffer(workspace, "workspace", pools.index))
     if check:
         _check(code, "ssm_cache_compact")
     return code

@@ -116,7 +116,7 @@ size_t ssm_gated_checkpoint_size(int batch, int dim, int64_t seqlen) {
 }
 
 ssm_status_t ssm_gated_scan_fwd(const ssm_gated_args_t* args, const ssm_gated_out_t* out, float* last_state, void* checkpoints,
-                                ssm_stream_t stream) {
+                                size_t checkpoint_bytes, ssm_stream_t stream) {
     GatedParams p;
     ssm_status_t st = common_params(args, &p);
     if (st != SSM_OK) return st;
@@ -129,6 +129,7 @@ ssm_status_t ssm_gated_scan_fwd(const ssm_gated_args_t* args, const ssm_gated_ou
     p.y = tensor(y, p.batch, p.dim);
     if (rows && p.L > 0 && !rows_apart(p.y, p.batch, p.dim, p.L)) return SSM_ERR_INVALID_ARG;
     if (!rows) return SSM_OK;
+    if (checkpoints && checkpoint_bytes < ssm_gated_checkpoint_size(p.batch, p.dim, p.L)) return SSM_ERR_WORKSPACE;
     int sms = 0;
     st = check_device(&sms);
     if (st != SSM_OK) return st;
@@ -152,7 +153,7 @@ size_t ssm_gated_bwd_workspace_size(int batch, int dim, int64_t seqlen, int have
 }
 
 ssm_status_t ssm_gated_scan_bwd(const ssm_gated_args_t* args, const ssm_gated_grads_t* grads, const void* checkpoints,
-                                void* workspace, size_t workspace_bytes, ssm_stream_t stream) {
+                                size_t checkpoint_bytes, void* workspace, size_t workspace_bytes, ssm_stream_t stream) {
     GatedParams p;
     ssm_status_t st = common_params(args, &p);
     if (st != SSM_OK) return st;
@@ -191,7 +192,8 @@ ssm_status_t ssm_gated_scan_bwd(const ssm_gated_args_t* args, const ssm_gated_gr
         return e == cudaSuccess ? SSM_OK : SSM_ERR_LAUNCH;
     }
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-        workspace_bytes < ssm_gated_bwd_workspace_size(p.batch, p.dim, p.L, checkpoints != nullptr))
+        workspace_bytes < ssm_gated_bwd_workspace_size(p.batch, p.dim, p.L, checkpoints != nullptr) ||
+        (checkpoints && checkpoint_bytes < ssm_gated_checkpoint_size(p.batch, p.dim, p.L)))
         return SSM_ERR_WORKSPACE;
     int sms = 0;
     st = check_device(&sms);

@@ -29,9 +29,9 @@ def declare(lib: ctypes.CDLL) -> None:
     lib.ssm_gated_checkpoint_size.restype = sz
     lib.ssm_gated_bwd_workspace_size.argtypes = [ci, ci, i64, ci]
     lib.ssm_gated_bwd_workspace_size.restype = sz
-    lib.ssm_gated_scan_fwd.argtypes = [st, st, vp, vp, vp]
+    lib.ssm_gated_scan_fwd.argtypes = [st, st, vp, vp, sz, vp]
     lib.ssm_gated_scan_fwd.restype = ci
-    lib.ssm_gated_scan_bwd.argtypes = [st, st, vp, vp, sz, vp]
+    lib.ssm_gated_scan_bwd.argtypes = [st, st, vp, sz, vp, sz, vp]
     lib.ssm_gated_scan_bwd.restype = ci
     lib.ssm_gated_state_update.argtypes = [st, vp]
     lib.ssm_gated_state_update.restype = ci
@@ -110,11 +110,12 @@ def _seq(t, name, x, dtype, shape, dev):
     """Address, batch stride and dim stride of a (batch, dim, seqlen) operand."""
     if t is None:
         return 0, 0, 0
-    at = _like(t, name, x, dtype, shape, dev)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _like(t, name, x, dtype, shape, dev)
     sb, sd, sl = t.stride()
     if sl != 1 and shape[2] > 1:
         raise ValueError(f"{name}: consecutive steps must be next to each other (stride {sl})")
-    return at, sb, sd
+    return t.data_ptr(), sb, sd
 
 
 def _io(x, dims):
@@ -154,14 +155,13 @@ def _args(like, r, i, lam, r_bias, i_bias, z, initial_state, lengths, reset, c):
                       _dense(lengths, "lengths", (b,), _I32, dev), _dense(reset, "reset", (b, L), _FLAG, dev), L, b, d, io, c)
 
 
-def _buffer(t, name, bytes_, dev):
+def _buffer(t, name, dev):
+    """Address and bytes of an optional dense buffer."""
     if t is None:
-        return 0
+        return 0, 0
     if not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"{name}: expected a dense tensor on cuda:{dev}")
-    if t.nbytes < bytes_:
-        raise ValueError(f"{name}: {t.nbytes} bytes, {bytes_} needed")
-    return t.data_ptr()
+    return t.data_ptr(), t.nbytes
 
 
 def ssm_gated_checkpoint_size(batch: int, dim: int, seqlen: int) -> int:
@@ -192,9 +192,8 @@ def ssm_gated_scan_fwd(x, r, i, lam, r_bias, i_bias, z, y, last_state, initial_s
     args = _args((x, dtype, shape, dev, io), r, i, lam, r_bias, i_bias, z, initial_state, lengths, reset, c)
     if y is None:
         raise ValueError("y is required")
-    ck = 0 if checkpoints is None else _buffer(checkpoints, "checkpoints", ssm_gated_checkpoint_size(*shape), dev)
     code = _call(dev, stream, _lib().ssm_gated_scan_fwd, args, _OUT.pack(*_seq(y, "y", x, dtype, shape, dev)),
-                 _dense(last_state, "last_state", shape[:2], _F32, dev), ck)
+                 _dense(last_state, "last_state", shape[:2], _F32, dev), *_buffer(checkpoints, "checkpoints", dev))
     if check:
         _check(code, "ssm_gated_scan_fwd")
     return code
@@ -213,9 +212,8 @@ def ssm_gated_scan_bwd(x, r, i, lam, r_bias, i_bias, z, dy, dx, dr, di, dlam, dr
                         *_seq(dr, "dr", *like), *_seq(di, "di", *like), *_seq(dz, "dz", *like), _dense(dlam, "dlam", ch, _F32, dev),
                         _dense(dr_bias, "dr_bias", ch, _F32, dev), _dense(di_bias, "di_bias", ch, _F32, dev),
                         _dense(dinitial_state, "dinitial_state", rows, _F32, dev))
-    ck = 0 if checkpoints is None else _buffer(checkpoints, "checkpoints", ssm_gated_checkpoint_size(*shape), dev)
-    code = _call(dev, stream, _lib().ssm_gated_scan_bwd, args, grads, ck, _buffer(workspace, "workspace", 0, dev),
-                 0 if workspace is None else workspace.nbytes)
+    code = _call(dev, stream, _lib().ssm_gated_scan_bwd, args, grads, *_buffer(checkpoints, "checkpoints", dev),
+                 *_buffer(workspace, "workspace", dev))
     if check:
         _check(code, "ssm_gated_scan_bwd")
     return code

@@ -24,14 +24,14 @@ def args(x=P, r=P, i=P, z=0, lam=P, r_bias=0, i_bias=0, h0=0, lengths=0, reset=0
     return gated._ARGS.pack(x, *st, r, *st, i, *st, z, *st, lam, r_bias, i_bias, h0, lengths, reset, L, b, d, io, c)
 
 
-def fwd(lib, y=2 * P, ys=(24, 8), last=None, ck=None, **kw):
-    return lib.ssm_gated_scan_fwd(args(**kw), gated._OUT.pack(y, *ys), last, ck, None)
+def fwd(lib, y=2 * P, ys=(24, 8), last=None, ck=None, ckb=1 << 20, **kw):
+    return lib.ssm_gated_scan_fwd(args(**kw), gated._OUT.pack(y, *ys), last, ck, ckb, None)
 
 
-def bwd(lib, dy=2 * P, dx=3 * P, dr=4 * P, di=5 * P, dz=0, dlam=0, ws=P, wsb=1 << 20, ds=(24, 8), ck=None, **kw):
+def bwd(lib, dy=2 * P, dx=3 * P, dr=4 * P, di=5 * P, dz=0, dlam=0, ws=P, wsb=1 << 20, ds=(24, 8), ck=None, ckb=1 << 20, **kw):
     st = (24, 8)
     g = gated._GRADS.pack(dy, *st, 0, dx, *ds, dr, *st, di, *st, dz, *st, dlam, 0, 0, 0)
-    return lib.ssm_gated_scan_bwd(args(**kw), g, ck, ws, wsb, None)
+    return lib.ssm_gated_scan_bwd(args(**kw), g, ck, ckb, ws, wsb, None)
 
 
 def test_forward_refusals(lib):
@@ -42,8 +42,9 @@ def test_forward_refusals(lib):
         assert fwd(lib, **bad) == IV, bad
     assert fwd(lib, b=65536, d=32768) == UN
     assert fwd(lib, L=(1 << 31) - 1024) == UN
-    assert lib.ssm_gated_scan_fwd(None, gated._OUT.pack(P, 24, 8), None, None, None) == IV
-    assert lib.ssm_gated_scan_fwd(args(), None, None, None, None) == IV
+    assert lib.ssm_gated_scan_fwd(None, gated._OUT.pack(P, 24, 8), None, None, 0, None) == IV
+    assert lib.ssm_gated_scan_fwd(args(), None, None, None, 0, None) == IV
+    assert fwd(lib, ck=P, ckb=16) == WS
     assert fwd(lib, b=0, x=0, r=0, i=0, y=0) == OK
     assert fwd(lib, d=0) == OK
 
@@ -56,7 +57,8 @@ def test_backward_refusals(lib):
     assert bwd(lib, ws=P + 16) == WS
     assert bwd(lib, wsb=16) == WS
     assert bwd(lib, d=0) == OK
-    assert lib.ssm_gated_scan_bwd(args(), None, None, P, 1 << 20, None) == IV
+    assert lib.ssm_gated_scan_bwd(args(), None, None, 0, P, 1 << 20, None) == IV
+    assert bwd(lib, ck=P, ckb=16) == WS
 
 
 def test_step_refusals(lib):

@@ -489,7 +489,8 @@ def test_refusals(cuda_device):
     refused(ValueError, lam=t["lam"].cpu())
     refused(ValueError, initial_state=torch.zeros(2, 10, device="cuda")[:, ::2])
     refused(ValueError, reset=torch.zeros(2, 17, dtype=torch.uint8, device="cuda"))
-    refused(ValueError, checkpoints=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    refused(binding.SsmError, checkpoints=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    refused(ValueError, checkpoints=torch.empty(1 << 16, dtype=torch.uint8))
     refused(binding.SsmError, c=-1.0)
     a = [t[k] for k in ("x", "r", "i", "lam", "r_bias", "i_bias", "z")]
     last = torch.empty(2, 5, device="cuda")
