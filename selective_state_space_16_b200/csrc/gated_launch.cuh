@@ -52,9 +52,9 @@ inline GatedShape split_shape(long long rows, int L, int steps, int sms, bool ba
 }
 
 template <typename IO>
-GatedShape gated_shape(long long rows, int L, int steps, int sms, bool backward) {
-    constexpr int kVec = 16 / sizeof(IO);
-    const long long need = L % kVec ? L + static_cast<long long>(kVec) - 1 : L;  // (rows then start anywhere in a vector)
+GatedShape gated_shape(long long rows, const ssm::GatedTensor& x, int L, int steps, int sms, bool backward) {
+    const unsigned long long at = (reinterpret_cast<uintptr_t>(x.p) / sizeof(IO)) | x.bs | x.ds | (16 / sizeof(IO));
+    const long long need = L + static_cast<long long>(16 / sizeof(IO) - (at & -at));  // (from the first row's vector on)
     int seg = 1;
     while (seg < 32 && static_cast<long long>(seg) * steps < need) seg *= 2;
     if (seg < 32) return {seg, 1, 1};
@@ -73,11 +73,21 @@ GatedKernel gated_kernel(GatedShape shape, bool backward) {
 template <typename IO>
 ssm_status_t launch_gated(ssm::GatedParams p, bool backward, int sms, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.batch) * p.dim;
-    const GatedShape shape = gated_shape<IO>(rows, p.L, backward ? ssm::kBwdSteps : ssm::kFwdSteps<IO>, sms, backward);
+    const GatedShape shape = gated_shape<IO>(rows, p.x, p.L, backward ? ssm::kBwdSteps : ssm::kFwdSteps<IO>, sms, backward);
     p.seg = shape.seg;
     p.split = shape.split;
     p.blocks = shape.blocks;
     const bool gate = p.z.p != nullptr, reset = p.reset != nullptr;
+    const auto alike = [](const ssm::GatedTensor& a, const ssm::GatedTensor& b) {
+        return a.bs == b.bs && a.ds == b.ds && ((reinterpret_cast<uintptr_t>(a.p) ^ reinterpret_cast<uintptr_t>(b.p)) & 15) == 0;
+    };
+    p.alike_in = alike(p.x, p.r) && alike(p.x, p.i) && (!gate || alike(p.x, p.z)) && (!backward || alike(p.x, p.dy));
+    p.alike_out = alike(p.dx, p.dr) && alike(p.dx, p.di) && (!gate || alike(p.dx, p.dz));
+    // 2^(31 + shift) / dim rounded up, 2^shift >= dim: off by less than 2^shift in it, so by less than 1 / dim in a
+    // quotient of rows below 2^31
+    p.dim_shift = 0;
+    while (1LL << p.dim_shift < p.dim) ++p.dim_shift;
+    p.dim_mul = static_cast<unsigned>(((1ULL << (31 + p.dim_shift)) + p.dim - 1) / p.dim);
     const GatedKernel kern = gate ? (reset ? gated_kernel<IO, true, true>(shape, backward) : gated_kernel<IO, true, false>(shape, backward))
                                   : (reset ? gated_kernel<IO, false, true>(shape, backward) : gated_kernel<IO, false, false>(shape, backward));
     const int block = shape.split > 1 ? shape.split / shape.blocks * 32 : ssm::kGatedWarps * 32;

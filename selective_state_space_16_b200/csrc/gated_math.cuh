@@ -33,6 +33,9 @@ struct GatedParams {
     int seg;     // lanes that share a row
     int split;   // warps that share a row (1: a row per warp or part of one)
     int blocks;  // blocks that those warps belong to, a cluster
+    bool alike_in, alike_out;  // the inputs, and the gradients, have the same strides and the same place in a vector
+    unsigned dim_mul;          // row / dim = row * dim_mul >> (31 + dim_shift)
+    int dim_shift;
     // backward
     GatedTensor dy, dx, dr, di, dz;
     const float* dlast;
@@ -259,13 +262,52 @@ struct Reach {
     int low, high;
 };
 
-// The row (b, d) of an input, which narrows the reach.
-template <typename IO>
-__device__ __forceinline__ const IO* row_in(const GatedTensor& t, int b, int d, Reach& reach) {
-    const long long at = b * t.bs + d * t.ds;
+__device__ __forceinline__ void narrow(Reach& reach, const GatedTensor& t, long long at) {
     reach.low = max(reach.low, -static_cast<int>(min(at, t.before)));
     reach.high = min(reach.high, static_cast<int>(min(t.most - at, t.before)));
-    return static_cast<const IO*>(t.p) + at;
+}
+
+__device__ __forceinline__ long long offset_of(const GatedTensor& t, int b, int d) { return b * t.bs + d * t.ds; }
+
+// The row (b, d) of operands that are `alike` or not, which narrows the reach.  A row's own work is some 300 to 500
+// instructions, as much as a tile: what can be found once for all operands is.
+template <typename IO, int N, typename... T>
+__device__ __forceinline__ void rows_of(bool alike, int b, int d, IO* (&row)[N], Reach& reach, const GatedTensor& t0, const T&... t) {
+    static_assert(sizeof...(T) + 1 == N, "a tensor for each row");
+    const long long at = offset_of(t0, b, d);
+    int k = 0;
+    if (alike) {
+        narrow(reach, t0, at);
+        row[0] = static_cast<IO*>(const_cast<void*>(t0.p)) + at;
+        ((row[++k] = static_cast<IO*>(const_cast<void*>(t.p)) + at), ...);
+    } else {
+        narrow(reach, t0, at);
+        row[0] = static_cast<IO*>(const_cast<void*>(t0.p)) + at;
+        ((narrow(reach, t, offset_of(t, b, d)), row[++k] = static_cast<IO*>(const_cast<void*>(t.p)) + offset_of(t, b, d)), ...);
+    }
+}
+
+// A row's groups are laid so that those of x start on 16-byte boundaries: group g holds the steps
+// from g * kGroup - phase.  Operands that lie like x, which dense ones of one shape do, are read and
+// written as vectors at any length of the rows; each operand is looked at by itself.
+template <typename IO>
+__device__ __forceinline__ int phase_of(const IO* row) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(IO));
+}
+
+// Which rows have their vectors where the groups have them.
+template <typename IO, int N>
+__device__ __forceinline__ bool in_phase(bool alike, IO* const (&row)[N], int phase, bool (&vec)[N]) {
+    bool all = phase_of(row[0]) == phase;
+    vec[0] = all;
+    if (alike) {
+#pragma unroll
+        for (int k = 1; k < N; ++k) vec[k] = vec[0];
+    } else {
+#pragma unroll
+        for (int k = 1; k < N; ++k) all &= vec[k] = phase_of(row[k]) == phase;
+    }
+    return all;
 }
 
 // Steps [t0, t0 + N) of the operands, those of them inside [0, len); the others are anything.
@@ -400,16 +442,21 @@ template <typename IO, int PAIRS>
 __device__ __forceinline__ void store_steps(IO* row, int t0, unsigned bits, bool vec, float2 (&v)[PAIRS]) {
     if (vec && bits == all_steps<2 * PAIRS>) {
         store_vectors(row, t0, v);
-    } else {
+    } else if (bits) {
+        IO* to = row + t0;
+        const unsigned words = sizeof(IO) == 2 && vec ? bits & bits >> 1 & 0x5555u : 0;  // pairs that are both inside
+        const unsigned rest = bits & ~(words * 3);
 #pragma unroll
         for (int k = 0; k < PAIRS; ++k) {
-            IO* to = row + t0 + 2 * k;
-            const unsigned two = bits >> (2 * k) & 3;
-            if (sizeof(IO) == 2 && vec && two == 3) {
-                *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(v[k].x, v[k].y);
+            if constexpr (sizeof(IO) == 2) {
+                const uint32_t w = pack_bf16x2(v[k].x, v[k].y);
+                unsigned short* half = reinterpret_cast<unsigned short*>(to) + 2 * k;
+                if (words >> (2 * k) & 1) *reinterpret_cast<uint32_t*>(half) = w;
+                if (rest >> (2 * k) & 1) half[0] = static_cast<unsigned short>(w);
+                if (rest >> (2 * k) & 2) half[1] = static_cast<unsigned short>(w >> 16);
             } else {
-                if (two & 1) to[0] = IoTraits<IO>::from_f32(v[k].x);
-                if (two & 2) to[1] = IoTraits<IO>::from_f32(v[k].y);
+                if (bits >> (2 * k) & 1) to[2 * k] = v[k].x;
+                if (bits >> (2 * k) & 2) to[2 * k + 1] = v[k].y;
             }
         }
     }
@@ -458,17 +505,13 @@ __device__ __forceinline__ bool flag_of(unsigned long long flags, int e) {
     return (static_cast<unsigned>(flags >> (e / 4 * 32)) & (0xffu << (e % 4 * 8))) != 0;
 }
 
-// A row's groups are laid so that those of x start on 16-byte boundaries: group g holds the steps
-// from g * kGroup - phase.  Operands that lie like x, which dense ones of one shape do, are read and
-// written as vectors at any length of the rows; each operand is looked at by itself.
-template <typename IO>
-__device__ __forceinline__ int phase_of(const IO* row) {
-    return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(IO));
-}
-
 template <typename IO>
 __device__ __forceinline__ IO* row_of(const GatedTensor& t, int b, int d) {
-    return static_cast<IO*>(const_cast<void*>(t.p)) + b * t.bs + d * t.ds;
+    return static_cast<IO*>(const_cast<void*>(t.p)) + offset_of(t, b, d);
+}
+
+__device__ __forceinline__ int batch_of(const GatedParams& p, unsigned row) {
+    return static_cast<int>(static_cast<unsigned long long>(row) * p.dim_mul >> (31 + p.dim_shift));
 }
 
 __device__ __forceinline__ int row_length(const GatedParams& p, int b) {

@@ -134,18 +134,24 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     const bool valid = at.row < static_cast<unsigned>(rows);
     if (SEG == 32 && !valid) return;  // (a whole warp)
     if (SPLIT && at.blocks > 1) cluster_arrive(), cluster_wait();  // every block has begun: its shared memory may be written
-    const int b = valid ? at.row / static_cast<unsigned>(p.dim) : 0, d = valid ? at.row - static_cast<unsigned>(b) * p.dim : 0;
+    const int b = valid ? batch_of(p, at.row) : 0, d = valid ? at.row - static_cast<unsigned>(b) * p.dim : 0;
     const int len = valid ? row_length(p, b) : 0;
     Reach reach{-15, 15};
-    const IO* in[kIn] = {row_in<IO>(p.x, b, d, reach), row_in<IO>(p.r, b, d, reach), row_in<IO>(p.i, b, d, reach)};
-    const IO* zrow[1] = {GATE ? row_in<IO>(p.z, b, d, reach) : nullptr};
+    const IO* in[kIn];
+    const IO* zrow[1];
+    if constexpr (GATE) {
+        const IO* row_in[kIn + 1];
+        rows_of(p.alike_in, b, d, row_in, reach, p.x, p.r, p.i, p.z);
+        in[0] = row_in[0], in[1] = row_in[1], in[2] = row_in[2], zrow[0] = row_in[3];
+    } else {
+        rows_of(p.alike_in, b, d, in, reach, p.x, p.r, p.i);
+    }
     reach.high += p.L;
     IO* y = p.y.p ? row_of<IO>(p.y, b, d) : nullptr;
     const int phase = phase_of(in[0]);
-    bool vec[kIn], all_vec = true;
-#pragma unroll
-    for (int k = 0; k < kIn; ++k) all_vec &= vec[k] = phase_of(in[k]) == phase;
-    const bool vy = phase_of(y) == phase, vz[1] = {phase_of(zrow[0]) == phase};
+    bool vec[kIn];
+    const bool all_vec = in_phase(p.alike_in, in, phase, vec);
+    const bool vy = phase_of(y) == phase, vz[1] = {GATE && (p.alike_in || phase_of(zrow[0]) == phase)};
     const unsigned char* reset = RESET ? p.reset + static_cast<long long>(b) * p.L : nullptr;
     const unsigned char* reset_end = RESET ? p.reset + static_cast<long long>(p.batch) * p.L : nullptr;
     const float root = sqrtf(2.f * p.c * softplus_lam(p.lam[d]));
@@ -160,7 +166,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
                                                   static_cast<unsigned>(p.x.bs) % n, static_cast<unsigned>(p.x.ds) % n, 0};
     }
 
-        int t0 = (at.part * at.seg + at.lane) * N - phase;
+    int t0 = (at.part * at.seg + at.lane) * N - phase;
     const int stride = at.parts * at.seg * N;
     Raw<IO, N> next[kIn];
     load_steps(in, vec, all_vec, t0, valid ? p.L : 0, reach, next);  // (not waiting for len)
@@ -265,20 +271,23 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     const bool valid = at.row < static_cast<unsigned>(rows);
     if (SEG == 32 && !valid) return;
     if (SPLIT && at.blocks > 1) cluster_arrive(), cluster_wait();
-    const int b = valid ? at.row / static_cast<unsigned>(p.dim) : 0, d = valid ? at.row - static_cast<unsigned>(b) * p.dim : 0;
+    const int b = valid ? batch_of(p, at.row) : 0, d = valid ? at.row - static_cast<unsigned>(b) * p.dim : 0;
     const int len = valid ? row_length(p, b) : 0, L = valid ? p.L : 0;
-    Reach reach{-15, 15};
-    const IO* in[kIn] = {row_in<IO>(p.x, b, d, reach), row_in<IO>(p.r, b, d, reach), row_in<IO>(p.i, b, d, reach), row_in<IO>(p.dy, b, d, reach)};
-    IO* out[kOut] = {row_of<IO>(p.dx, b, d), row_of<IO>(p.dr, b, d), row_of<IO>(p.di, b, d)};
-    if (GATE) in[kIn - 1] = row_in<IO>(p.z, b, d, reach), out[kOut - 1] = row_of<IO>(p.dz, b, d);
+    Reach reach{-15, 15}, any{0, 0};
+    const IO* in[kIn];
+    IO* out[kOut];
+    if constexpr (GATE) {
+        rows_of(p.alike_in, b, d, in, reach, p.x, p.r, p.i, p.dy, p.z);
+        rows_of(p.alike_out, b, d, out, any, p.dx, p.dr, p.di, p.dz);
+    } else {
+        rows_of(p.alike_in, b, d, in, reach, p.x, p.r, p.i, p.dy);
+        rows_of(p.alike_out, b, d, out, any, p.dx, p.dr, p.di);
+    }
     reach.high += p.L;
     const CkptHeader where = *reinterpret_cast<const CkptHeader*>(p.ckpt);
     const int phase = static_cast<int>((where.base + b * where.bs + d * where.ds) % (16 / sizeof(IO)));
-    bool vin[kIn], vout[kOut], all_vec = true;
-#pragma unroll
-    for (int k = 0; k < kIn; ++k) all_vec &= vin[k] = phase_of(in[k]) == phase;
-#pragma unroll
-    for (int k = 0; k < kOut; ++k) all_vec &= vout[k] = phase_of(out[k]) == phase;
+    bool vin[kIn], vout[kOut];
+    const bool in_vec = in_phase(p.alike_in, in, phase, vin), all_vec = in_phase(p.alike_out, out, phase, vout) && in_vec;
     const unsigned char* reset = RESET ? p.reset + static_cast<long long>(b) * p.L : nullptr;
     const unsigned char* reset_end = RESET ? p.reset + static_cast<long long>(p.batch) * p.L : nullptr;
     const float* ckpt = p.ckpt + sizeof(CkptHeader) / 4 + row * p.ckpt_row;
@@ -290,7 +299,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     float2 sumT = both(0.f), sumr = both(0.f), sumi = both(0.f);
 
     const int stride = at.parts * at.seg * N;
-    int t = (len + phase + stride - 1) / stride * stride - phase;  // where the rounds with steps end
+    int t = ((len + phase + stride - 1) & -stride) - phase;  // where the rounds with steps end (stride: a power of two)
     for (int t0 = t + (at.part * at.seg + at.lane) * N; t0 < L; t0 += stride) {  // padding: zeros
         float2 zero[kPairs] = {};
 #pragma unroll
@@ -469,9 +478,11 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
             store_vectors(out[1], t0, kr);
             store_vectors(out[2], t0, ki);
         } else if (active) {
+            if (len < L) {
 #pragma unroll
-            for (int e = 0; e < N; ++e)  // (0 times an infinite gradient of the last state)
-                if (!(inside >> e & 1)) step_of(kx, e) = step_of(kr, e) = step_of(ki, e) = 0.f;
+                for (int e = 0; e < N; ++e)  // (0 times an infinite gradient of the last state)
+                    if (!(inside >> e & 1)) step_of(kx, e) = step_of(kr, e) = step_of(ki, e) = 0.f;
+            }
             const unsigned to = steps_inside<N>(t0, L);
             store_steps(out[0], t0, to, vout[0], kx);
             store_steps(out[1], t0, to, vout[1], kr);
