@@ -269,8 +269,9 @@ __device__ __forceinline__ void narrow(Reach& reach, const GatedTensor& t, long 
 
 __device__ __forceinline__ long long offset_of(const GatedTensor& t, int b, int d) { return b * t.bs + d * t.ds; }
 
-// The row (b, d) of operands that are `alike` or not, which narrows the reach.  A row's own work is some 300 to 500
-// instructions, as much as a tile: what can be found once for all operands is.
+// The row (b, d) of operands that are `alike` or not, which narrows the reach.  A row's own work is as many
+// instructions as a tile: finding what alike operands share once took 16 x 5120 rows of 250 steps, forward and backward,
+// from 238 to 225 us.
 template <typename IO, int N, typename... T>
 __device__ __forceinline__ void rows_of(bool alike, int b, int d, IO* (&row)[N], Reach& reach, const GatedTensor& t0, const T&... t) {
     static_assert(sizeof...(T) + 1 == N, "a tensor for each row");

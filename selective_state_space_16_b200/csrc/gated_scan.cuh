@@ -7,19 +7,19 @@
 // scan in one direction only, and dx, dr, di, dz and the parameters' sums leave the same pass.
 //
 // SEG = 32: a warp per row.  SEG = 0: p.seg lanes per row, 1 to 16: several short rows per warp, so that few
-// lanes idle (16 x 5120 rows of 100 steps, forward and backward: 295 -> 141 us).
+// lanes idle (16 x 5120 rows of 100 steps, forward and backward: 129 us, 295 with a warp each).
 // SPLIT: the warps of a block, or of a cluster of blocks, share one row: of p.split warps in all each takes
 // every p.split-th tile, and a barrier a round joins their pairs, which every warp writes into the shared
 // memory of all blocks of the cluster.  That is for few long rows, which could not fill the GPU's warps
-// otherwise (64 rows of 32768 steps: 60 -> 33 us).
+// otherwise (64 rows of 32768 steps: 33 us, 60 with 4 warps of a block).
 //
 // What bounds it (bf16 with the gate, B200): the bytes, and close behind them the special-function unit (5
 // operations a step forward: two exponentials, a reciprocal root, a reciprocal, a tanh) and issue (about 30
-// instructions a step forward, 65 backward, packed fp32 pairs throughout).  32768 steps of 5120 channels: 308 us,
-// 83% of the copy rate; forward 2048 steps of 8 x 1536 channels 50 us (77%), backward 82 us (87%), with
-// resets 56 and 100; fp32 the pair at 84%.  What was slower: the forward's operands through the backward's
+// instructions a step forward, 65 backward, packed fp32 pairs throughout, and some 300 and 400 a row).  32768 steps
+// of 5120 channels: 317 us, 81% of the copy rate; 2048 steps of 8 x 1536 channels, forward and backward, 143 us
+// (75%), with resets 158 (68%), fp32 248 (87%).  What was slower: the forward's operands through the backward's
 // ring (334 us); warps that stay and take the next row's first tile under way (backward 106 us: registers);
-// reset flags a tile ahead (+6 us).
+// reset flags a tile ahead (+6 us); a later row's first tile fetched into L2 by the warp before (no gain, or 2%).
 #pragma once
 
 #include <type_traits>

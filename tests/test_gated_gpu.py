@@ -231,6 +231,51 @@ def test_operands_of_every_alignment(cuda_device, io):
             assert bool(torch.isfinite(v).all()) and base.shape[0] > 0
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [37, 100, 250, 700])
+@pytest.mark.parametrize("one", [None, "i", "z", "dy", "dr", "dz"])
+def test_operands_that_lie_alike(cuda_device, io, L, one):
+    """All inputs alike and all gradients alike, each at an odd place, but for `one` of them; what lies beside their
+    rows stays."""
+    B, D = 3, 7
+    t, dy, dlast = inputs(B, D, L, io, seed=L)
+    inp = dict(t, dy=dy)
+    names = ("x", "r", "i", "z", "dy"), ("dx", "dr", "di", "dz")
+    wide = {}
+
+    def placed(k, by, pad):
+        by, pad = (by + 1, pad + 2) if k == one else (by, pad)
+        flat = torch.full((B * D * (L + pad) + by + 16,), 7.0, dtype=dy.dtype, device="cuda")
+        wide[k] = flat
+        return flat[by:by + B * D * (L + pad)].view(B, D, L + pad)[..., :L]
+
+    for k in names[0]:
+        v = placed(k, 3, 1)
+        v.copy_(inp[k])
+        inp[k] = v
+    out = {k: placed(k, 5, 3) for k in names[1]}
+    dy = inp.pop("dy")
+    ck, ws = ssm.new_gated_checkpoints(B, D, L), ssm.new_gated_workspace(B, D, L)
+    a = [inp[k] for k in ("x", "r", "i", "lam", "r_bias", "i_bias", "z")]
+    y, last, dh0 = torch.empty(B, D, L, dtype=dy.dtype, device="cuda"), torch.empty(B, D, device="cuda"), torch.empty(B, D, device="cuda")
+    sums = [torch.empty(D, device="cuda") for _ in range(3)]
+    ssm.ssm_gated_scan_fwd(*a, y, last, initial_state=inp["initial_state"], checkpoints=ck)
+    ssm.ssm_gated_scan_bwd(*a, dy, out["dx"], out["dr"], out["di"], *sums, out["dz"], ws, initial_state=inp["initial_state"],
+                           dlast_state=dlast, dinitial_state=dh0, checkpoints=ck)
+    got = dict(out, y=y, last=last, dinitial_state=dh0, **dict(zip(("dlam", "dr_bias", "di_bias"), sums)))
+    compare(got, t, dy, dlast, f"alike but {one}")
+    for k, v in wide.items():
+        view = inp[k] if k in inp else out.get(k, dy)
+        view.fill_(7.0)
+        assert bool((v == 7).all()), f"{k}: written beside its rows"
+
+
+@pytest.mark.parametrize("B,D,L", [(1, 70001, 2), (9001, 1, 3), (1500, 2, 5), (5, 4099, 1), (3, 4097, 17), (129, 127, 9)])
+def test_many_short_rows(cuda_device, B, D, L):
+    t, dy, dlast = inputs(B, D, L, "bf16", lengths=[1 + k % L for k in range(B)], seed=B)
+    compare(run_all(t, dy, dlast, True), t, dy, dlast, f"{B}x{D}x{L}")
+
+
 def test_transposed_batch_and_channels(cuda_device):
     """Strides of (dim, batch, seqlen) tensors."""
     t, dy, dlast = inputs(3, 5, 290, "bf16", seed=17)
