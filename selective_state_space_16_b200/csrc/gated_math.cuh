@@ -270,8 +270,8 @@ __device__ __forceinline__ void narrow(Reach& reach, const GatedTensor& t, long 
 __device__ __forceinline__ long long offset_of(const GatedTensor& t, int b, int d) { return b * t.bs + d * t.ds; }
 
 // The row (b, d) of operands that are `alike` or not, which narrows the reach.  A row's own work is as many
-// instructions as a tile: finding what alike operands share once took 16 x 5120 rows of 250 steps, forward and backward,
-// from 238 to 225 us.
+// instructions as a tile, so what alike operands share is found once (with row / dim as a product: backward of
+// 16 x 5120 rows of 250 steps 173 -> 170 us).
 template <typename IO, int N, typename... T>
 __device__ __forceinline__ void rows_of(bool alike, int b, int d, IO* (&row)[N], Reach& reach, const GatedTensor& t0, const T&... t) {
     static_assert(sizeof...(T) + 1 == N, "a tensor for each row");
@@ -438,7 +438,8 @@ __device__ __forceinline__ unsigned steps_inside(int t0, int n) {
     return bits;
 }
 
-// The steps at the bits; `vec`: as a vector where that is all of them.
+// The steps at the bits; `vec`: as a vector where that is all of them.  A row's ends: each word and element under its
+// own bit, without a branch (backward of 16 x 5120 rows of 101 steps 104 -> 94 us).
 template <typename IO, int PAIRS>
 __device__ __forceinline__ void store_steps(IO* row, int t0, unsigned bits, bool vec, float2 (&v)[PAIRS]) {
     if (vec && bits == all_steps<2 * PAIRS>) {
