@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     }
     reach.high += p.L;
     IO* y = p.y.p ? row_of<IO>(p.y, b, d) : nullptr;
-    const int phase = phase_of(in[0]);
+    const int phase = valid ? phase_of(in[0]) : 0;  // (lanes without a row, of length 0: no step lies before that)
     bool vec[kIn];
     const bool all_vec = in_phase(p.alike_in, in, phase, vec);
     const bool vy = phase_of(y) == phase, vz[1] = {GATE && (p.alike_in || phase_of(zrow[0]) == phase)};
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     }
     reach.high += p.L;
     const CkptHeader where = *reinterpret_cast<const CkptHeader*>(p.ckpt);
-    const int phase = static_cast<int>((where.base + b * where.bs + d * where.ds) % (16 / sizeof(IO)));
+    const int phase = valid ? static_cast<int>((where.base + b * where.bs + d * where.ds) % (16 / sizeof(IO))) : 0;
     bool vin[kIn], vout[kOut];
     const bool in_vec = in_phase(p.alike_in, in, phase, vin), all_vec = in_phase(p.alike_out, out, phase, vout) && in_vec;
     const unsigned char* reset = RESET ? p.reset + static_cast<long long>(b) * p.L : nullptr;

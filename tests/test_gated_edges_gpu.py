@@ -1,0 +1,57 @@
+"""The gated linear recurrence at its edges (-m gpu): what lies behind the buffers it is given, steps outside a row
+beside infinities and NaNs, the output gate, the ends of the parameters' range."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_16_b200 as ssm
+from gated_reference import check, reference
+from test_gated_gpu import IO, compare, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+def off_vectors(v, by):
+    """The same values, `by` elements behind a 16-byte boundary."""
+    flat = torch.empty(v.numel() + by + 16, dtype=v.dtype, device=v.device)
+    at = flat[by:by + v.numel()].view(v.shape)
+    return at.copy_(v)
+
+
+def guarded(nbytes):
+    """A buffer of that many bytes, and the sentinels behind it."""
+    whole = torch.full((nbytes + 65536,), 0x5a, dtype=torch.uint8, device="cuda")
+    return whole[:nbytes], whole[nbytes:]
+
+
+def forward_backward(t, dy, dlast, ck, ws, ck_bwd):
+    B, D, L = t["x"].shape
+    a = [t[k] for k in ("x", "r", "i", "lam", "r_bias", "i_bias", "z")]
+    more = dict(initial_state=t["initial_state"], lengths=t["lengths"], reset=t["reset"])
+    y, last, dh0 = torch.zeros(B, D, L, dtype=dy.dtype, device="cuda"), torch.empty(B, D, device="cuda"), torch.empty(B, D, device="cuda")
+    out = {k: torch.empty(B, D, L, dtype=dy.dtype, device="cuda") for k in ("dx", "dr", "di")}
+    out["dz"] = None if t["z"] is None else torch.empty_like(out["dx"])
+    sums = [torch.empty(D, device="cuda") for _ in range(3)]
+    ssm.ssm_gated_scan_fwd(*a, y, last, checkpoints=ck, **more)
+    ssm.ssm_gated_scan_bwd(*a, dy, out["dx"], out["dr"], out["di"], *sums, out["dz"], ws, dlast_state=dlast, dinitial_state=dh0,
+                           checkpoints=ck_bwd, **more)
+    return dict(out, y=y, last=last, dinitial_state=dh0, **dict(zip(("dlam", "dr_bias", "di_bias"), sums)))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("by", [1, 3])
+@pytest.mark.parametrize("B,D", [(1, 1), (1, 5), (3, 7)])
+@pytest.mark.parametrize("L", [1, 5, 37, 100])
+def test_nothing_behind_the_buffers_is_written(cuda_device, io, by, B, D, L):
+    """Short rows that do not fill a block, off the 16-byte boundaries: checkpoints and workspace of exactly the sizes
+    that the library asks for."""
+    t, dy, dlast = inputs(B, D, L, io, seed=L + by)
+    for k in ("x", "r", "i", "z"):
+        t[k] = off_vectors(t[k], by)
+    dy = off_vectors(dy, by)
+    ck, behind_ck = guarded(ssm.ssm_gated_checkpoint_size(B, D, L))
+    for given in (True, False):
+        ws, behind_ws = guarded(ssm.ssm_gated_bwd_workspace_size(B, D, L, given))
+        got = forward_backward(t, dy, dlast, ck, ws, ck if given else None)
+        assert bool((behind_ck == 0x5a).all()) and bool((behind_ws == 0x5a).all())
+        compare(got, t, dy, dlast, f"{B}x{D}x{L} off by {by}")
