@@ -55,3 +55,67 @@ def test_nothing_behind_the_buffers_is_written(cuda_device, io, by, B, D, L):
         got = forward_backward(t, dy, dlast, ck, ws, ck if given else None)
         assert bool((behind_ck == 0x5a).all()) and bool((behind_ws == 0x5a).all())
         compare(got, t, dy, dlast, f"{B}x{D}x{L} off by {by}")
+
+
+def with_and_without_checkpoints(t, dy, dlast):
+    """The results, which are the same bit for bit whether the backward has the forward's checkpoints or makes its own."""
+    sizes = t["x"].shape
+    ck = ssm.new_gated_checkpoints(*sizes)
+    got, own = (forward_backward(t, dy, dlast, ck, ssm.new_gated_workspace(*sizes, g is not None), g) for g in (ck, None))
+    for k, v in got.items():
+        assert v is own[k] or torch.equal(v.view(torch.uint8), own[k].view(torch.uint8)), k
+    return got
+
+
+EDGES = [(2, 3, 701), (2, 3, 37), (3, 7, 101), (2, 600, 301), (2, 3, 9001)]  # rows split, shared warps, a warp each, clusters
+
+
+def set_rows(v, rows):
+    for b, value in enumerate(rows):
+        if value is not None:
+            v[b] = value
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("B,D,L", EDGES)
+@pytest.mark.parametrize("before", [float("nan"), float("inf")])
+def test_what_came_before_a_first_reset_reaches_no_gradient(cuda_device, io, B, D, L, before):
+    """A reset at step 0 drops the initial state, wherever the rows lie: the parameters' sums too."""
+    t, dy, dlast = inputs(B, D, L, io, reset=0.01, seed=L)
+    t["reset"][:, 0] = 1
+    t["initial_state"][:] = before
+    got = with_and_without_checkpoints(t, dy, dlast)
+    compare(got, t, dy, dlast, f"{B}x{D}x{L}")
+    assert all(bool(torch.isfinite(v).all()) for v in got.values())
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("B,D,L", EDGES)
+@pytest.mark.parametrize("state,dstate", [(float("nan"), None), (float("inf"), None), (None, float("inf")), (None, float("nan"))])
+def test_rows_without_steps_reach_no_sum(cuda_device, io, B, D, L, state, dstate):
+    """A batch row of length 0 hands its state and the state's gradient on and has no part in anything else."""
+    t, dy, dlast = inputs(B, D, L, io, lengths=[L - 2, 0] + [7] * (B - 2), seed=L)
+    set_rows(t["initial_state"], [None, state])
+    set_rows(dlast, [None, dstate])
+    got = with_and_without_checkpoints(t, dy, dlast)
+    compare(got, t, dy, dlast, f"{B}x{D}x{L}")
+    assert all(bool(torch.isfinite(got[k]).all()) for k in ("dlam", "dr_bias", "di_bias"))
+    for k in ("dx", "dr", "di", "dz"):
+        assert not bool(got[k][1].any()), k
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("B,D,L", EDGES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_gradients_behind_a_row_are_zeros_beside_any_state(cuda_device, io, B, D, L, bad):
+    """A row whose last step, a reset, leaves a state that is not finite: behind it are zeros, and the sums that
+    this step does not enter stay finite."""
+    n = L - 3
+    t, dy, dlast = inputs(B, D, L, io, lengths=[n] * B, reset=0.0, seed=L)
+    t["reset"][:, n - 1] = 1
+    t["x"][0, :, n - 1] = bad
+    got = with_and_without_checkpoints(t, dy, dlast)
+    for k in ("dx", "dr", "di", "dz"):
+        assert not bool(got[k][:, :, n:].any()), k
+    compare(got, t, dy, dlast, f"{B}x{D}x{L}")
+    assert all(bool(torch.isfinite(got[k]).all()) for k in ("dlam", "dr_bias"))
