@@ -13,10 +13,10 @@
 // memory of all blocks of the cluster.  That is for few long rows, which could not fill the GPU's warps
 // otherwise (64 rows of 32768 steps: 33 us, 60 with 4 warps of a block).
 //
-// What bounds it (bf16 with the gate, B200): the bytes, and close behind them the special-function unit (5
-// operations a step forward: two exponentials, a reciprocal root, a reciprocal, a tanh) and issue (about 30
+// What bounds it (bf16 with the gate, B200): the bytes, and close behind them the special-function unit (6
+// operations a step forward: three exponentials, a reciprocal root, two reciprocals) and issue (about 30
 // instructions a step forward, 65 backward, packed fp32 pairs throughout, and some 300 and 400 a row).  32768 steps
-// of 5120 channels: 317 us, 81% of the copy rate; 2048 steps of 8 x 1536 channels, forward and backward, 143 us
+// of 5120 channels: 335 us, 76% of the copy rate; 2048 steps of 8 x 1536 channels, forward and backward, 143 us
 // (75%), with resets 158 (68%), fp32 248 (87%).  What was slower: the forward's operands through the backward's
 // ring (334 us); warps that stay and take the next row's first tile under way (backward 106 us: registers);
 // reset flags a tile ahead (+6 us); a later row's first tile fetched into L2 by the warp before (no gain, or 2%).
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
         if (GATE) {
             unpack<IO, N>(zc[0], w);
 #pragma unroll
-            for (int k = 0; k < kPairs; ++k) u[k] = __fmul2_rn(u[k], gate_silu2<IO>(w[k]));
+            for (int k = 0; k < kPairs; ++k) u[k] = __fmul2_rn(u[k], silu2(w[k]));
         }
         if (y) store_steps(y, t0, inside, vy, u);
     }

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepBlocks) gated_step_kernel(c
                 const Gate gate = gate_of(__fadd2_rn(two_of(w.i, k), ib[k]), 0.f);
                 y[k] = __ffma2_rn(dec.a, two_of(w.h, k), __fmul2_rn(__fmul2_rn(dec.m, gate.sig), two_of(w.x, k)));
                 w.h.w[2 * k] = __float_as_uint(y[k].x), w.h.w[2 * k + 1] = __float_as_uint(y[k].y);
-                if (GATE) y[k] = __fmul2_rn(y[k], gate_silu2<IO>(two_of(w.z, k)));
+                if (GATE) y[k] = __fmul2_rn(y[k], silu2(two_of(w.z, k)));
             }
         };
         if (near)

@@ -119,3 +119,22 @@ def test_gradients_behind_a_row_are_zeros_beside_any_state(cuda_device, io, B, D
         assert not bool(got[k][:, :, n:].any()), k
     compare(got, t, dy, dlast, f"{B}x{D}x{L}")
     assert all(bool(torch.isfinite(got[k]).all()) for k in ("dlam", "dr_bias"))
+
+
+@pytest.mark.parametrize("low,high", [(-1.0, 1.0), (-20.0, -1.0), (1.0, 20.0), (-90.0, -60.0)])
+def test_the_output_gate_is_right_to_the_rounding_of_bf16(cuda_device, low, high):
+    """y of bf16 is the value in 32 bits rounded once: within that value's bound and half a step, 2^-8 of it, far on
+    the gate's shut side too (the rounding is of a value that may be off by the bound: hence the product)."""
+    t, _, _ = inputs(2, 24, 500, "bf16", seed=73)
+    t["z"] = torch.linspace(low, high, 2 * 24 * 500, device="cuda").view(2, 24, 500).to(torch.bfloat16)
+    val, err = reference(**t)["y"]
+    tol = err * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(val)
+    y, _ = ssm.gated_scan_fwd(**t)
+    check(y, (val, tol), f"gate {low} .. {high}")
+    state = torch.zeros(1, 24, device="cuda").expand(2, 24).clone()
+    cols = [t[k][..., 3].contiguous() for k in ("x", "r", "i", "z")]
+    y = torch.empty(2, 24, dtype=torch.bfloat16, device="cuda")
+    ssm.ssm_gated_state_update(state, *cols[:3], t["lam"], t["r_bias"], t["i_bias"], cols[3], y)
+    one = {k: t[k][..., 3:4] for k in ("x", "r", "i", "z")}
+    val, err = reference(**dict(t, **one, initial_state=None))["y"]
+    check(y[..., None], (val, err * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(val)), "gate of a step")
