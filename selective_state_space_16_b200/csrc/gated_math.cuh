@@ -94,6 +94,13 @@ __device__ __forceinline__ float softplus_lam(float lam) {
     return fmaf(e, p, fmaxf(lam, 0.f));
 }
 
+// sqrt(2 c softplus(lam)), the root of twice a channel's largest decay exponent, as far as that is an fp32 number: a
+// shut gate multiplies it by 0.  (At the bound a = 0 and m = 1 for any open gate.)
+__device__ __forceinline__ float root_of(float c, float lam) {
+    const float root = sqrtf(2.f * (c * softplus_lam(lam)));
+    return root > 1.8e19f ? 1.8e19f : root;
+}
+
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // 1 + y P(y) for the polynomials of gated_poly.cuh, for two steps.

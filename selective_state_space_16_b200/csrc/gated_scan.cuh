@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     const bool vy = phase_of(y) == phase, vz[1] = {GATE && (p.alike_in || phase_of(zrow[0]) == phase)};
     const unsigned char* reset = RESET ? p.reset + static_cast<long long>(b) * p.L : nullptr;
     const unsigned char* reset_end = RESET ? p.reset + static_cast<long long>(p.batch) * p.L : nullptr;
-    const float root = sqrtf(2.f * p.c * softplus_lam(p.lam[d]));
+    const float root = root_of(p.c, p.lam[d]);
     const bool near = root <= kNear;
     const float rb = bounded(-kLog2e * (p.r_bias ? p.r_bias[d] : 0.f)), ib = -kLog2e * (p.i_bias ? p.i_bias[d] : 0.f);
     float carry = p.h0 && valid ? p.h0[row] : 0.f;
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(SPLIT ? kMaxSplit * 32 : kGatedWarps * 32, SPL
     const unsigned char* reset = RESET ? p.reset + static_cast<long long>(b) * p.L : nullptr;
     const unsigned char* reset_end = RESET ? p.reset + static_cast<long long>(p.batch) * p.L : nullptr;
     const float* ckpt = p.ckpt + sizeof(CkptHeader) / 4 + row * p.ckpt_row;
-    const float root = sqrtf(2.f * p.c * softplus_lam(p.lam[d]));
+    const float root = root_of(p.c, p.lam[d]);
     const bool near = root <= kNear;
     const float rb = bounded(-kLog2e * (p.r_bias ? p.r_bias[d] : 0.f)), ib = -kLog2e * (p.i_bias ? p.i_bias[d] : 0.f);
     float carry = p.dlast && valid ? p.dlast[row] : 0.f;  // a_{t+1} g_{t+1}: what the steps after the tile send back

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepBlocks) gated_step_kernel(c
     bool near = true;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        root[k] = make_float2(sqrtf(2.f * p.c * softplus_lam(root[k].x)), sqrtf(2.f * p.c * softplus_lam(root[k].y)));
+        root[k] = make_float2(root_of(p.c, root[k].x), root_of(p.c, root[k].y));
         near &= root[k].x <= kNear && root[k].y <= kNear;
     }
     near = __all_sync(0xffffffffu, near);

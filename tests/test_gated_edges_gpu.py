@@ -138,3 +138,36 @@ def test_the_output_gate_is_right_to_the_rounding_of_bf16(cuda_device, low, high
     one = {k: t[k][..., 3:4] for k in ("x", "r", "i", "z")}
     val, err = reference(**dict(t, **one, initial_state=None))["y"]
     check(y[..., None], (val, err * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(val)), "gate of a step")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("B,D,L", EDGES)
+def test_decay_exponents_beyond_fp32(cuda_device, io, B, D, L):
+    """c softplus(lam) past the largest fp32 forgets at once (a = 0, m = 1), and steps outside a row, whose gate is
+    shut, still pass the state on."""
+    t, dy, dlast = inputs(B, D, L, io, lengths=[L - 3] * B, seed=L)
+    y, last = ssm.gated_scan_fwd(**t, c=3e38)
+    grads = ssm.gated_scan_bwd(**t, dy=dy, dlast_state=dlast, c=3e38)
+    want = reference(**t, dy=dy, dlast=dlast, c=3e38, bf16=io == "bf16")
+    for k, w in want.items():
+        check(dict(grads, y=y, last=last)[k], w, f"c=3e38 {k}")
+    some, all_ = (dict(t, lam=torch.full((D,), v, device="cuda")) for v in (1e30, float("inf")))
+    for a, b in zip(ssm.gated_scan_fwd(**some), ssm.gated_scan_fwd(**all_)):
+        assert torch.equal(a, b) and bool(torch.isfinite(a).all())
+    some, all_ = (ssm.gated_scan_bwd(**w, dy=dy, dlast_state=dlast) for w in (some, all_))
+    for k, v in some.items():
+        assert torch.equal(v, all_[k]) and bool(torch.isfinite(v).all()), k
+    frozen = ssm.gated_scan_fwd(**dict(t, lam=torch.full((D,), -200.0, device="cuda")), c=3e38)[1]  # c softplus(lam) is 0
+    assert torch.equal(frozen, t["initial_state"])
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_a_shut_gate_keeps_the_state_of_any_channel_in_a_step(cuda_device, io):
+    x = torch.randn(3, 40, device="cuda").to(IO[io])
+    shut = torch.full_like(x, float("-inf"))
+    lam = torch.linspace(-9, 3, 40, device="cuda")
+    lam[:20] = 1e38
+    state = torch.randn(3, 40, device="cuda")
+    keep, y = state.clone(), torch.empty_like(x)
+    ssm.ssm_gated_state_update(state, x, shut, x, lam, None, None, None, y)
+    assert torch.equal(state, keep)
