@@ -16,7 +16,7 @@
  * allocated, calls asynchronous on `stream`, status codes), and:
  *   - x, r, i, z, y and their gradients have io_dtype elements (fp32 or bf16), shape (batch, dim,
  *     seqlen) with consecutive steps next to each other; the batch and channel strides are given
- *     (in elements), so that slices of a wider tensor, such as the three parts of one
+ *     (in elements; those of an input may be zero or negative), so that slices of a wider tensor, such as the three parts of one
  *     projection's output, are taken as they are.  Any alignment of the elements' own size.  What lies
  *     between an operand's first and last row has to be readable memory: a few elements beside a row may
  *     be read with it (and are never used).

@@ -48,7 +48,7 @@ long long checkpoint_row(int64_t seqlen) {
 template <typename T>
 GatedTensor tensor(const T& t, int batch, int dim) {
     const bool up = t.batch_stride >= 0 && t.dim_stride >= 0;
-    return {t.data, t.batch_stride, t.dim_stride, (batch - 1LL) * t.batch_stride + (dim - 1LL) * t.dim_stride, up ? 15 : 0};
+    return {t.data, t.batch_stride, t.dim_stride, (batch - 1LL) * t.batch_stride + (dim - 1LL) * t.dim_stride, up ? 15ull : 0ull};
 }
 
 bool element_aligned(const void* p, int io) {

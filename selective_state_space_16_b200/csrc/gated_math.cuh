@@ -17,7 +17,7 @@ struct GatedTensor {
     const void* p;
     long long bs, ds;
     long long most;    // where the last row starts
-    long long before;  // elements beside a row that may be read where the operand has them: 15, or 0 (odd strides)
+    unsigned long long before;  // elements beside a row that may be read where the operand has them: 15, or 0 (rows backwards)
 };
 
 struct GatedParams {
@@ -257,9 +257,10 @@ struct Reach {
     int low, high;
 };
 
-__device__ __forceinline__ void narrow(Reach& reach, const GatedTensor& t, long long at) {
-    reach.low = max(reach.low, -static_cast<int>(min(at, t.before)));
-    reach.high = min(reach.high, static_cast<int>(min(t.most - at, t.before)));
+__host__ __device__ __forceinline__ void narrow(Reach& reach, const GatedTensor& t, long long at) {
+    // (unsigned, so that places before the address, where `before` is 0, do not wrap)
+    reach.low = max(reach.low, -static_cast<int>(min(static_cast<unsigned long long>(at), t.before)));
+    reach.high = min(reach.high, static_cast<int>(min(static_cast<unsigned long long>(t.most - at), t.before)));
 }
 
 __device__ __forceinline__ long long offset_of(const GatedTensor& t, int b, int d) { return b * t.bs + d * t.ds; }

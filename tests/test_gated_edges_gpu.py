@@ -6,6 +6,7 @@ import torch
 
 import selective_state_space_16_b200 as ssm
 from gated_reference import check, reference
+from selective_state_space_16_b200 import binding, gated
 from test_gated_gpu import IO, compare, inputs
 
 pytestmark = pytest.mark.gpu
@@ -171,3 +172,25 @@ def test_a_shut_gate_keeps_the_state_of_any_channel_in_a_step(cuda_device, io):
     keep, y = state.clone(), torch.empty_like(x)
     ssm.ssm_gated_state_update(state, x, shut, x, lam, None, None, None, y)
     assert torch.equal(state, keep)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [37, 100, 301])
+def test_rows_that_go_backwards_in_memory(cuda_device, io, L):
+    """Inputs of negative strides, which the C ABI takes.  (A row is composed in groups that lie on 16 bytes, so the same row
+    elsewhere is the same to the bound, not to the bit.)"""
+    B, D = 3, 7
+    t, _, _ = inputs(B, D, L, io, seed=L)
+    want = reference(**t, bf16=io == "bf16")
+    y, last = torch.empty_like(t["x"]), torch.empty(B, D, device="cuda")
+    packed, kept = [], []
+    for k in ("x", "r", "i", "z"):
+        kept.append(t[k].flip(0, 1).contiguous())
+        packed += [kept[-1].data_ptr() + ((B - 1) * D + D - 1) * L * kept[-1].element_size(), -D * L, -L]
+    args = gated._ARGS.pack(*packed, *(t[k].data_ptr() for k in ("lam", "r_bias", "i_bias", "initial_state")), 0, 0, L, B, D,
+                            binding.SSM_BF16 if io == "bf16" else binding.SSM_F32, 8.0)
+    code = ssm.load().ssm_gated_scan_fwd(args, gated._OUT.pack(y.data_ptr(), D * L, L), last.data_ptr(), None, 0,
+                                         torch.cuda.current_stream().cuda_stream)
+    assert code == binding.SSM_OK
+    check(y, want["y"], "y")
+    check(last, want["last"], "last")
