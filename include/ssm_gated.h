@@ -29,8 +29,8 @@
  *     a packed row begins: a_t = 0 and m_t = 1, so that h_t = iota_t x_t whatever came before
  *     (infinities and NaNs included), and no gradient passes back over the border.
  *   - An output may not be the same buffer as an input, nor may its own rows overlap (both
- *     SSM_ERR_INVALID_ARG); it must not overlap another
- *     argument; initial_state and last_state of the forward may be the same buffer.
+ *     SSM_ERR_INVALID_ARG); it must not overlap another argument.  Only a state's two ends may be
+ *     the same buffer: initial_state and last_state, dlast_state and dinitial_state.
  *   - Every sum is formed in a fixed order: repeated calls give identical results.
  *   - batch * dim < 2^31, seqlen < 2^31 - 65536 (SSM_ERR_UNSUPPORTED).
  */

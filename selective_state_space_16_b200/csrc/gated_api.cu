@@ -99,7 +99,12 @@ bool rows_apart(const GatedTensor& t, int batch, int dim, int64_t L) {
 }
 
 bool is_input(const ssm_gated_args_t* a, const void* q) {
-    return q && (q == a->x.data || q == a->r.data || q == a->i.data || q == a->z.data);
+    if (!q) return false;
+    for (const void* in : {a->x.data, a->r.data, a->i.data, a->z.data, static_cast<const void*>(a->lam), static_cast<const void*>(a->r_bias),
+                           static_cast<const void*>(a->i_bias), static_cast<const void*>(a->initial_state),
+                           static_cast<const void*>(a->lengths), static_cast<const void*>(a->reset)})
+        if (q == in) return true;
+    return false;
 }
 
 ssm_status_t launch_fwd(int io, const GatedParams& p, int sms, cudaStream_t s) {
@@ -125,6 +130,7 @@ ssm_status_t ssm_gated_scan_fwd(const ssm_gated_args_t* args, const ssm_gated_ou
     const bool rows = p.batch > 0 && p.dim > 0;
     if (rows && p.L > 0 && !y.data) return SSM_ERR_INVALID_ARG;
     if (is_input(args, y.data) || !element_aligned(y.data, args->io_dtype)) return SSM_ERR_INVALID_ARG;
+    if (last_state != args->initial_state && is_input(args, last_state)) return SSM_ERR_INVALID_ARG;
     if (!float_aligned(last_state) || !aligned16(checkpoints)) return SSM_ERR_INVALID_ARG;
     p.y = tensor(y, p.batch, p.dim);
     if (rows && p.L > 0 && !rows_apart(p.y, p.batch, p.dim, p.L)) return SSM_ERR_INVALID_ARG;
@@ -163,7 +169,11 @@ ssm_status_t ssm_gated_scan_bwd(const ssm_gated_args_t* args, const ssm_gated_gr
     if (rows && p.L > 0 && (!g.dy.data || !g.dx.data || !g.dr.data || !g.di.data || (args->z.data && !g.dz.data)))
         return SSM_ERR_INVALID_ARG;
     for (const void* q : {g.dx.data, g.dr.data, g.di.data, g.dz.data})
-        if (is_input(args, q) || (q && q == g.dy.data) || !element_aligned(q, args->io_dtype)) return SSM_ERR_INVALID_ARG;
+        if (!element_aligned(q, args->io_dtype)) return SSM_ERR_INVALID_ARG;
+    for (const void* q : {g.dx.data, g.dr.data, g.di.data, g.dz.data, static_cast<void*>(g.dlam), static_cast<void*>(g.dr_bias),
+                          static_cast<void*>(g.di_bias)})
+        if (is_input(args, q) || (q && (q == g.dy.data || q == g.dlast_state))) return SSM_ERR_INVALID_ARG;
+    if (is_input(args, g.dinitial_state) || (g.dinitial_state && g.dinitial_state == g.dy.data)) return SSM_ERR_INVALID_ARG;
     if (!element_aligned(g.dy.data, args->io_dtype) || !aligned16(checkpoints)) return SSM_ERR_INVALID_ARG;
     for (const void* q : {static_cast<const void*>(g.dlast_state), static_cast<const void*>(g.dlam), static_cast<const void*>(g.dr_bias),
                           static_cast<const void*>(g.di_bias), static_cast<const void*>(g.dinitial_state)})
@@ -186,7 +196,7 @@ ssm_status_t ssm_gated_scan_bwd(const ssm_gated_args_t* args, const ssm_gated_gr
         for (float* q : {g.dlam, g.dr_bias, g.di_bias})
             if (q && e == cudaSuccess) e = cudaMemsetAsync(q, 0, static_cast<size_t>(p.dim) * sizeof(float), s);
         const size_t bytes = static_cast<size_t>(p.batch) * p.dim * sizeof(float);
-        if (g.dinitial_state && bytes && e == cudaSuccess)
+        if (g.dinitial_state && bytes && g.dinitial_state != g.dlast_state && e == cudaSuccess)
             e = g.dlast_state ? cudaMemcpyAsync(g.dinitial_state, g.dlast_state, bytes, cudaMemcpyDeviceToDevice, s)
                               : cudaMemsetAsync(g.dinitial_state, 0, bytes, s);
         return e == cudaSuccess ? SSM_OK : SSM_ERR_LAUNCH;

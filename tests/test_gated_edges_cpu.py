@@ -3,10 +3,17 @@ import os
 import subprocess
 
 import pytest
+import torch
 
-from selective_state_space_16_b200 import build
+import selective_state_space_16_b200 as ssm
+from selective_state_space_16_b200 import binding, build, gated
 
 CSRC = build.CSRC
+
+
+@pytest.fixture(autouse=True, scope="module")
+def built():
+    build.build()
 
 REACH = r"""
 #include <cstdio>
@@ -57,3 +64,38 @@ def test_no_row_reaches_outside_its_operand(reach):
     for r, g, w in zip(rows, got, want):
         assert w[0] <= g[0] and g[1] <= w[1], (r, g, w)  # not outside
         assert g == w or not r[3], (r, g, w)                       # and as far as it may
+
+
+def test_an_output_may_be_no_input():
+    """As the header says: not even a parameter, a state or a list.  (initial_state and last_state may be one buffer, and
+    dlast_state and dinitial_state.)"""
+    lib, ok = ssm.load(), binding.SSM_ERR_LAUNCH  # (accepted arguments get as far as the device, which is not here)
+    P = 1 << 20
+    ins = {k: P * (j + 1) for j, k in enumerate(("x", "r", "i", "z", "lam", "r_bias", "i_bias", "h0", "lengths", "reset"))}
+    B, D, L = 2, 3, 8
+    st = (D * L, L)
+
+    def args():
+        return gated._ARGS.pack(ins["x"], *st, ins["r"], *st, ins["i"], *st, ins["z"], *st, *(ins[k] for k in (
+            "lam", "r_bias", "i_bias", "h0", "lengths", "reset")), L, B, D, binding.SSM_F32, 8.0)
+
+    def fwd(y=50 * P, last=51 * P):
+        return lib.ssm_gated_scan_fwd(args(), gated._OUT.pack(y, *st), last, None, 0, None)
+
+    def bwd(dy=60 * P, dlast=61 * P, **out):
+        o = dict({k: P * (70 + j) for j, k in enumerate(("dx", "dr", "di", "dz", "dlam", "drb", "dib", "dh0"))}, **out)
+        g = gated._GRADS.pack(dy, *st, dlast, o["dx"], *st, o["dr"], *st, o["di"], *st, o["dz"], *st, o["dlam"], o["drb"], o["dib"], o["dh0"])
+        return lib.ssm_gated_scan_bwd(args(), g, None, 0, 90 * P, 1 << 20, None)
+
+    if torch.cuda.is_available():
+        pytest.skip("accepted calls would run on these addresses")
+    assert fwd() == ok and fwd(last=ins["h0"]) == ok and fwd(last=0) == ok
+    assert bwd() == ok and bwd(dh0=61 * P) == ok and bwd(dh0=0, dlam=0, drb=0, dib=0) == ok
+    for k, p in ins.items():
+        assert fwd(y=p) == binding.SSM_ERR_INVALID_ARG, k
+        assert fwd(last=p) == (ok if k == "h0" else binding.SSM_ERR_INVALID_ARG), k
+        for out in ("dx", "dr", "di", "dz", "dlam", "drb", "dib", "dh0"):
+            assert bwd(**{out: p}) == binding.SSM_ERR_INVALID_ARG, (out, k)
+    for out in ("dx", "dr", "di", "dz", "dlam", "drb", "dib", "dh0"):
+        assert bwd(**{out: 60 * P}) == binding.SSM_ERR_INVALID_ARG, out
+        assert bwd(**{out: 61 * P}) == (ok if out == "dh0" else binding.SSM_ERR_INVALID_ARG), out

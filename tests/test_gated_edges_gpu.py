@@ -194,3 +194,15 @@ def test_rows_that_go_backwards_in_memory(cuda_device, io, L):
     assert code == binding.SSM_OK
     check(y, want["y"], "y")
     check(last, want["last"], "last")
+
+
+@pytest.mark.parametrize("B,D,L", EDGES + [(2, 3, 0)])
+def test_the_states_gradient_may_stay_in_its_buffer(cuda_device, B, D, L):
+    """dinitial_state over dlast_state, as a backward taken block by block carries it."""
+    t, dy, dlast = inputs(B, D, L, "bf16", lengths=[L, 0] + [L // 2] * (B - 2), seed=79)
+    want = ssm.gated_scan_bwd(**t, dy=dy, dlast_state=dlast)["dinitial_state"]
+    a = [t[k] for k in ("x", "r", "i", "lam", "r_bias", "i_bias", "z")]
+    out = [torch.empty_like(dy) for _ in range(4)]
+    ssm.ssm_gated_scan_bwd(*a, dy, *out[:3], None, None, None, out[3], ssm.new_gated_workspace(B, D, L), initial_state=t["initial_state"],
+                           lengths=t["lengths"], dlast_state=dlast, dinitial_state=dlast)
+    assert torch.equal(dlast, want)
