@@ -32,7 +32,8 @@
  *     SSM_ERR_INVALID_ARG); it must not overlap another argument.  Only a state's two ends may be
  *     the same buffer: initial_state and last_state, dlast_state and dinitial_state.
  *   - Every sum is formed in a fixed order: repeated calls give identical results.
- *   - batch * dim < 2^31, seqlen < 2^31 - 65536 (SSM_ERR_UNSUPPORTED).
+ *   - batch * dim < 2^31, seqlen < 2^31 - 65536; a one-token step: batch <= 65535, dim < 2^31 - 65536
+ *     (else SSM_ERR_UNSUPPORTED).
  */
 #ifndef SSM_GATED_H
 #define SSM_GATED_H

@@ -35,8 +35,11 @@ __global__ void __launch_bounds__(128) gated_bwd_params_kernel(const float* part
 
 bool valid_sizes(int batch, int dim, int64_t seqlen) { return batch >= 0 && dim >= 0 && seqlen >= 0; }
 
+constexpr long long kMaxSteps = (1LL << 31) - (1 << 16);  // (steps are 32-bit in the kernels, a few tiles past the last)
+constexpr int kMaxStepBatch = 65535;  // (far past a batch of a decode step)
+
 bool supported_sizes(int batch, int dim, int64_t seqlen) {
-    return static_cast<long long>(batch) * dim < (1LL << 31) && seqlen < (1LL << 31) - (1 << 16);  // (steps are 32-bit in the kernels)
+    return static_cast<long long>(batch) * dim < (1LL << 31) && seqlen < kMaxSteps;
 }
 
 // Floats of a row of checkpoints: one for each group of steps, of which the first can begin up to
@@ -252,7 +255,7 @@ ssm_status_t ssm_gated_state_update(const ssm_gated_step_t* args, ssm_stream_t s
     for (const void* q : {static_cast<const void*>(a.state), static_cast<const void*>(a.slots), static_cast<const void*>(a.lam),
                           static_cast<const void*>(a.r_bias), static_cast<const void*>(a.i_bias)})
         if (!float_aligned(q)) return SSM_ERR_INVALID_ARG;
-    if (a.batch > 65535) return SSM_ERR_UNSUPPORTED;  // the batch row is a grid y index
+    if (a.batch > kMaxStepBatch || a.dim >= kMaxSteps) return SSM_ERR_UNSUPPORTED;
     int sms = 0;
     const ssm_status_t st = check_device(&sms);
     if (st != SSM_OK) return st;

@@ -99,3 +99,16 @@ def test_an_output_may_be_no_input():
     for out in ("dx", "dr", "di", "dz", "dlam", "drb", "dib", "dh0"):
         assert bwd(**{out: 60 * P}) == binding.SSM_ERR_INVALID_ARG, out
         assert bwd(**{out: 61 * P}) == (ok if out == "dh0" else binding.SSM_ERR_INVALID_ARG), out
+
+
+def test_limits_of_a_step():
+    """batch at most 65535, dim below 2^31 - 65536: refused before any device is asked for."""
+    def step(b, d):
+        P = 1 << 20
+        return ssm.load().ssm_gated_state_update(gated._STEP.pack(P, d, 0, 2 * P, 2 * P, 2 * P, 0, 3 * P, d, d, d, d, d, P, 0, 0, b, d, b,
+                                                                  binding.SSM_BF16, 8.0), None)
+    if torch.cuda.is_available():
+        pytest.skip("accepted calls would run on these addresses")
+    assert step(65535, 8) == step(1, (1 << 31) - 65537) == binding.SSM_ERR_LAUNCH  # (accepted: no device)
+    for b, d in ((65536, 8), (1, (1 << 31) - 65536), (1, (1 << 31) - 1)):
+        assert step(b, d) == binding.SSM_ERR_UNSUPPORTED, (b, d)
