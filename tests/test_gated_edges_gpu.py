@@ -7,7 +7,7 @@ import torch
 import selective_state_space_16_b200 as ssm
 from gated_reference import check, reference
 from selective_state_space_16_b200 import binding, gated
-from test_gated_gpu import IO, compare, inputs
+from test_gated_gpu import IO, compare, inputs, step_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -206,3 +206,69 @@ def test_the_states_gradient_may_stay_in_its_buffer(cuda_device, B, D, L):
     ssm.ssm_gated_scan_bwd(*a, dy, *out[:3], None, None, None, out[3], ssm.new_gated_workspace(B, D, L), initial_state=t["initial_state"],
                            lengths=t["lengths"], dlast_state=dlast, dinitial_state=dlast)
     assert torch.equal(dlast, want)
+
+
+def beside(v):
+    """The elements of v's buffer that are not v's, as a copy with v's filled in."""
+    keep = v.clone()
+    v.fill_(7.0)
+    whole = v._base.clone()
+    v.copy_(keep)
+    return whole
+
+
+def placed(shape, dtype, by, pad):
+    """A tensor that starts `by` elements into a buffer of sevens and has `pad` of them between its rows."""
+    flat = torch.full((shape[0] * shape[1] * (shape[2] + pad) + by + 64,), 7.0, dtype=dtype, device="cuda")
+    return flat.as_strided(shape, (shape[1] * (shape[2] + pad), shape[2] + pad, 1), by)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [5, 37, 100, 250, 541])
+@pytest.mark.parametrize("first,second", [((3, 1), (0, 0)), ((0, 0), (5, 2)), ((1, 8), (6, 1))])
+def test_checkpoints_go_by_position(cuda_device, io, L, first, second):
+    """The checkpoints of a forward are read by a backward whose operands lie at other addresses and strides; what lies
+    beside the outputs' rows stays."""
+    B, D = 3, 7
+    t, dy, dlast = inputs(B, D, L, io, lengths=[L, L // 2, 1], seed=L)
+    ck, ws = ssm.new_gated_checkpoints(B, D, L), ssm.new_gated_workspace(B, D, L, True)
+    y, last, dh0 = placed(dy.shape, dy.dtype, *first), torch.empty(B, D, device="cuda"), torch.empty(B, D, device="cuda")
+    y.zero_()
+    a = {k: placed(dy.shape, dy.dtype, *first).copy_(t[k]) for k in ("x", "r", "i", "z")}
+    more = dict(initial_state=t["initial_state"], lengths=t["lengths"])
+    ssm.ssm_gated_scan_fwd(a["x"], a["r"], a["i"], t["lam"], t["r_bias"], t["i_bias"], a["z"], y, last, checkpoints=ck, **more)
+    a = {k: placed(dy.shape, dy.dtype, *second).copy_(t[k]) for k in ("x", "r", "i", "z")}
+    out = {k: placed(dy.shape, dy.dtype, by, pad) for k, by, pad in (("dx", 7, 1), ("dr", 1, 0), ("di", 0, 8), ("dz", 9, 7))}
+    sums = [torch.empty(D, device="cuda") for _ in range(3)]
+    ssm.ssm_gated_scan_bwd(a["x"], a["r"], a["i"], t["lam"], t["r_bias"], t["i_bias"], a["z"], dy, out["dx"], out["dr"], out["di"], *sums,
+                           out["dz"], ws, dlast_state=dlast, dinitial_state=dh0, checkpoints=ck, **more)
+    got = dict(out, y=y, last=last, dinitial_state=dh0, **dict(zip(("dlam", "dr_bias", "di_bias"), sums)))
+    compare(got, t, dy, dlast, f"L={L}")
+    for k in ("y", *out):
+        assert bool((beside(got[k]) == 7).all()), f"{k}: written beside its rows"
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("B,D", [(200, 8192), (2000, 600), (3000, 37)])
+@pytest.mark.parametrize("kind", ["distinct", "repeated", "none"])
+def test_steps_of_many_rows_per_block(cuda_device, io, B, D, kind):
+    """More rows than a launch has blocks for, so that each block walks several: slots in any order with padding
+    rows among them, slots named again by rows of the same block and of others, and rows without slots."""
+    t, _, _ = inputs(B, D, 1, io, seed=B + D)
+    g = torch.Generator().manual_seed(B)
+    n = {"distinct": B + 50, "repeated": B // 8, "none": B - 9}[kind]  # (none: the last rows have no state)
+    at = list(range(B)) if kind == "none" else torch.randperm(n, generator=g)[:B].tolist() if kind == "distinct" else \
+        torch.randint(0, n, (B,), generator=g).tolist()
+    if kind != "none":
+        at[3::11] = [-1] * len(at[3::11])
+        at[-1], at[7] = n, -(2 ** 31)
+    state = torch.randn(n, D, generator=g).cuda()
+    y0, ey, st, est = step_reference(t, state, at, 0, io == "bf16")
+    y = torch.full((B, D), 5.0, dtype=IO[io], device="cuda")
+    cols = [t[k][..., 0].contiguous() for k in ("x", "r", "i", "z")]
+    ssm.ssm_gated_state_update(state, *cols[:3], t["lam"], t["r_bias"], t["i_bias"], cols[3], y,
+                               slots=None if kind == "none" else torch.tensor(at, dtype=torch.int32, device="cuda"))
+    skipped = np.isnan(y0[:, 0])
+    assert bool((y[torch.from_numpy(skipped).cuda()] == 5).all())
+    check(y[torch.from_numpy(~skipped).cuda()], (y0[~skipped], ey[~skipped]), "y")
+    check(state, (st, est), "state")
