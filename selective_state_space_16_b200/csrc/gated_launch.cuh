@@ -17,9 +17,9 @@ struct GatedShape {
     int seg, split, blocks;
 };
 
-// How full the waves of 16 warps per SM are, if each of `warps` is a warp's work.
-inline double wave_fill(long long warps, int sms) {
-    const double waves = static_cast<double>(warps) / (16. * sms);
+// How full the waves of `resident` warps are, if each of `warps` is a warp's work.
+inline double wave_fill(long long warps, long long resident) {
+    const double waves = static_cast<double>(warps) / static_cast<double>(resident);
     return waves / std::ceil(waves);
 }
 
@@ -29,11 +29,14 @@ inline double wave_fill(long long warps, int sms) {
 // 47 and 47 (4 x 4); 200 x 16384 45 with 4, 43 with 8, 43 with 4 x 2 blocks; 300 x 16384 53 with 4, 57 with 8, 64 with
 // 4 x 2; 768 x 16384 121, 92, 92 and 100 with 1, 2, 4 and 8; 1536 x 8192 86 and 93 with 1 and 2.  3 or 6 warps took
 // longer than 2 and 4 throughout.
-// Long rows in a few waves are split too where that fills the last wave better by enough to pay for the barriers:
+// Long rows in a few waves (`alone`: the warps of an SM with a row each; 16 with rows split) are split too where
+// that fills the last wave better by enough to pay for the barriers:
 // under a steady load, at the clock that the power cap leaves, us with 1 and 2 or 4 warps: fp32 forward 5120 x 16384
 // 315 and 294, bf16 3000 x 16384 106 and 102, backward 2600 x 8192 89 and 87, forward 55 and 50; but bf16 forward 5120 x
 // 32768 324 and 326, 12288 x 8192 193 and 199.  Rows of 4 tiles lose: 12288 x 2048 64, 76 and 94 with 1, 2 and 4.
-inline GatedShape split_shape(long long rows, int L, int steps, int sms, bool backward, bool f32) {
+// The fp32 backward, 12 warps alone, rows of 8192 steps with 1 and 2: 2000 rows 127 and 112, 2368 136 and 132, 2600 145
+// and 146, 3003 157 and 164, 3300 164 and 173, 4000 217 and 209 (not taken, as 4700: 238 and 237).
+inline GatedShape split_shape(long long rows, int L, int steps, int sms, bool backward, bool f32, int alone) {
     const long long tiles = (L + 32LL * steps - 1) / (32 * steps);
     int warps = 1, blocks = 1;
     while (rows * warps * blocks < 8LL * sms && warps * blocks < tiles) {
@@ -44,9 +47,11 @@ inline GatedShape split_shape(long long rows, int L, int steps, int sms, bool ba
         else
             break;
     }
-    if (rows > 16LL * sms)
+    const long long split = 2LL * ssm::kMaxSplit * sms;
+    if (rows > static_cast<long long>(alone) * sms)
         while (warps < (backward ? 2 : 4) && tiles >= (backward ? 16 : 8) * warps * warps &&
-               wave_fill(rows * warps * 2, sms) > (f32 && !backward ? 1.06 : 1.3) * wave_fill(rows * warps, sms))
+               wave_fill(rows * warps * 2, split) >
+                   (f32 && !backward ? 1.06 : 1.3) * wave_fill(rows * warps, warps > 1 ? split : static_cast<long long>(alone) * sms))
             warps *= 2;
     return {32, warps * blocks, blocks};
 }
@@ -60,7 +65,7 @@ GatedShape gated_shape(long long rows, const ssm::GatedTensor& x, int L, int ste
     int seg = 1;
     while (seg < 32 && static_cast<long long>(seg) * steps < need) seg *= 2;
     if (seg < 32) return {seg, 1, 1};
-    return split_shape(rows, L, steps, sms, backward, sizeof(IO) == 4);
+    return split_shape(rows, L, steps, sms, backward, sizeof(IO) == 4, ssm::kGatedWarps * (backward ? ssm::kBwdBlocks<IO> : ssm::kFwdBlocks));
 }
 
 using GatedKernel = void (*)(const ssm::GatedParams);

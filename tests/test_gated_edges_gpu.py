@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import selective_state_space_16_b200 as ssm
+import test_gated_gpu
 from gated_reference import check, reference
 from selective_state_space_16_b200 import binding, gated
 from test_gated_gpu import IO, compare, inputs, step_reference
@@ -272,3 +273,9 @@ def test_steps_of_many_rows_per_block(cuda_device, io, B, D, kind):
     assert bool((y[torch.from_numpy(skipped).cuda()] == 5).all())
     check(y[torch.from_numpy(~skipped).cuda()], (y0[~skipped], ey[~skipped]), "y")
     check(state, (st, est), "state")
+
+
+@pytest.mark.parametrize("io,D", [("f32", 1800), ("f32", 2368), ("bf16", 1800), ("bf16", 2400)])
+def test_rows_around_a_wave(cuda_device, io, D):
+    """As many long rows as the GPU holds warps of a kernel, and a few more or less: a warp each or two."""
+    test_gated_gpu.test_many_long_rows(cuda_device, io, D, 4100)
