@@ -31,7 +31,8 @@
  *   - An output may not be the same buffer as an input, nor may its own rows overlap (both
  *     SSM_ERR_INVALID_ARG); it must not overlap another argument.  Only a state's two ends may be
  *     the same buffer: initial_state and last_state, dlast_state and dinitial_state.
- *   - Every sum is formed in a fixed order: repeated calls give identical results.
+ *   - Every sum is formed in a fixed order: repeated calls give identical results.  (A row is taken in groups that
+ *     lie on 16 bytes, so the same row at another offset from them may differ in its last bits.)
  *   - batch * dim < 2^31, seqlen < 2^31 - 65536; a one-token step: batch <= 65535, dim < 2^31 - 65536
  *     (else SSM_ERR_UNSUPPORTED).
  */

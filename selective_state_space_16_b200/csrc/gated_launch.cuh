@@ -25,15 +25,15 @@ inline double wave_fill(long long warps, long long resident) {
 
 // Splitting goes on, by twos, until the GPU has 8 warps per SM (16 are resident) or a round covers the row: up to
 // 4 warps of one block, then with fewer rows than SMs up to 8 blocks, else up to 8 warps.  Forward and backward of
-// bf16 rows with a gate, us: 64 x 32768 60 with 4 warps, 44 with 16 in a block, 33 with 4 x 8 blocks; 128 x 32768 61,
-// 47 and 47 (4 x 4); 200 x 16384 45 with 4, 43 with 8, 43 with 4 x 2 blocks; 300 x 16384 53 with 4, 57 with 8, 64 with
-// 4 x 2; 768 x 16384 121, 92, 92 and 100 with 1, 2, 4 and 8; 1536 x 8192 86 and 93 with 1 and 2.  3 or 6 warps took
+// bf16 rows with a gate, us: 64 x 32768 58 with 4 warps, 43 with 8, 32 with 4 x 4 blocks, 27 with 4 x 8; 128 x 32768 62,
+// 46, 44 and 54; 200 x 16384 42 with 4, 38 with 8, 37 with 4 x 2 blocks; 300 x 16384 51 with 4, 55 with 8, 61 with
+// 4 x 2; 768 x 16384 122, 93, 92 and 98 with 1, 2, 4 and 8; 1536 x 8192 85 and 90 with 1 and 2.  3 or 6 warps took
 // longer than 2 and 4 throughout.
 // Long rows in a few waves (`alone`: the warps of an SM with a row each; 16 with rows split) are split too where
 // that fills the last wave better by enough to pay for the barriers:
-// under a steady load, at the clock that the power cap leaves, us with 1 and 2 or 4 warps: fp32 forward 5120 x 16384
-// 315 and 294, bf16 3000 x 16384 106 and 102, backward 2600 x 8192 89 and 87, forward 55 and 50; but bf16 forward 5120 x
-// 32768 324 and 326, 12288 x 8192 193 and 199.  Rows of 4 tiles lose: 12288 x 2048 64, 76 and 94 with 1, 2 and 4.
+// us with 1, 2 and 4 warps: fp32 forward 5120 x 16384 311, 293 and 287, bf16 3000 x 16384 107, 106 and 105, 2600 x 8192 53,
+// 48 and 49, backward 87 with 1 and 2; but bf16 forward 5120 x 32768 332, 339 and 338, 12288 x 8192 197 and 206 with 1
+// and 2.  Rows of 4 tiles lose: 12288 x 2048 56, 63 and 84.
 // The fp32 backward, 12 warps alone, rows of 8192 steps with 1 and 2: 2000 rows 127 and 112, 2368 136 and 132, 2600 145
 // and 146, 3003 157 and 164, 3300 164 and 173, 4000 217 and 209 (not taken, as 4700: 238 and 237).
 inline GatedShape split_shape(long long rows, int L, int steps, int sms, bool backward, bool f32, int alone) {
@@ -57,7 +57,7 @@ inline GatedShape split_shape(long long rows, int L, int steps, int sms, bool ba
 }
 
 // A row begins anywhere that its strides and address allow in a 16-byte vector; its lanes count from the vector's
-// begin (bf16 forward of 16 x 5120 rows of 250 steps: 70 us on half warps, 131 on whole ones).
+// begin (bf16 forward of 16 x 5120 rows of 250 steps: 67 us on half warps, 114 on whole ones).
 template <typename IO>
 GatedShape gated_shape(long long rows, const ssm::GatedTensor& x, int L, int steps, int sms, bool backward) {
     const unsigned long long at = (reinterpret_cast<uintptr_t>(x.p) / sizeof(IO)) | x.bs | x.ds | (16 / sizeof(IO));

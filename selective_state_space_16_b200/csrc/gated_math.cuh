@@ -52,14 +52,14 @@ struct CkptHeader {
 constexpr int kGroup = 8;  // steps between two checkpoints
 
 // Steps that a lane holds at once.  bf16 forward: 16 (two 16-byte vectors of each operand) halve the shuffles
-// and the tile's own work per step; 32768 steps of 5120 channels 330 us with 8 (96 registers), 305 with 16.
+// and the tile's own work per step; 32768 steps of 5120 channels 408 us with 8, 331 with 16.
 // fp32, and the backward with six values kept per step: 8.
 template <typename IO> constexpr int kFwdSteps = sizeof(IO) == 2 ? 16 : 8;
 constexpr int kBwdSteps = 8;
 
-// Stages of the backward's ring.  Forward and backward, us: 8 x 1536 x 2048 bf16 166 with 2 or 3, 168 with 4, 182
-// without a ring; fp32 254 without, 246 with 2, 244 with 3, but 64 x 32768 fp32 47, 43 and 55 (shared memory for fewer
-// blocks).
+// Stages of the backward's ring.  Forward and backward, us: 8 x 1536 x 2048 bf16 153, 151 and 151 with 2, 3 and 4 (a tenth
+// more without a ring, on an earlier form); fp32 253, 250 and 256, but 64 x 32768 fp32 40, 52 and 53 (shared memory for
+// fewer blocks).
 template <typename IO> constexpr int kBwdStages = sizeof(IO) == 2 ? 3 : 2;
 
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -266,8 +266,8 @@ __host__ __device__ __forceinline__ void narrow(Reach& reach, const GatedTensor&
 __device__ __forceinline__ long long offset_of(const GatedTensor& t, int b, int d) { return b * t.bs + d * t.ds; }
 
 // The row (b, d) of operands that are `alike` or not, which narrows the reach.  A row's own work is as many
-// instructions as a tile, so what alike operands share is found once (with row / dim as a product: backward of
-// 16 x 5120 rows of 250 steps 173 -> 170 us).
+// instructions as a tile, so what alike operands share is found once (with row / dim as a product: 2% of the backward
+// of 16 x 5120 rows of 250 steps).
 template <typename IO, int N, typename... T>
 __device__ __forceinline__ void rows_of(bool alike, int b, int d, IO* (&row)[N], Reach& reach, const GatedTensor& t0, const T&... t) {
     static_assert(sizeof...(T) + 1 == N, "a tensor for each row");
@@ -435,7 +435,7 @@ __device__ __forceinline__ unsigned steps_inside(int t0, int n) {
 }
 
 // The steps at the bits; `vec`: as a vector where that is all of them.  A row's ends: each word and element under its
-// own bit, without a branch (backward of 16 x 5120 rows of 101 steps 104 -> 94 us).
+// own bit, without a branch (a tenth of the backward of 16 x 5120 rows of 101 steps).
 template <typename IO, int PAIRS>
 __device__ __forceinline__ void store_steps(IO* row, int t0, unsigned bits, bool vec, float2 (&v)[PAIRS]) {
     if (vec && bits == all_steps<2 * PAIRS>) {

@@ -7,19 +7,24 @@
 // scan in one direction only, and dx, dr, di, dz and the parameters' sums leave the same pass.
 //
 // SEG = 32: a warp per row.  SEG = 0: p.seg lanes per row, 1 to 16: several short rows per warp, so that few
-// lanes idle (16 x 5120 rows of 100 steps, forward and backward: 129 us, 295 with a warp each).
+// lanes idle (16 x 5120 rows of 100 steps, forward and backward: 127 us, 264 with a warp each).
 // SPLIT: the warps of a block, or of a cluster of blocks, share one row: of p.split warps in all each takes
 // every p.split-th tile, and a barrier a round joins their pairs, which every warp writes into the shared
 // memory of all blocks of the cluster.  That is for few long rows, which could not fill the GPU's warps
-// otherwise (64 rows of 32768 steps: 33 us, 60 with 4 warps of a block).
+// otherwise (64 rows of 32768 steps: 27 us, 58 with 4 warps of a block).
 //
-// What bounds it (bf16 with the gate, B200): the bytes, and close behind them the special-function unit (6
-// operations a step forward: three exponentials, a reciprocal root, two reciprocals) and issue (about 30
-// instructions a step forward, 65 backward, packed fp32 pairs throughout, and some 300 and 400 a row).  32768 steps
-// of 5120 channels: 335 us, 76% of the copy rate; 2048 steps of 8 x 1536 channels, forward and backward, 143 us
-// (75%), with resets 158 (68%), fp32 248 (87%).  What was slower: the forward's operands through the backward's
-// ring (334 us); warps that stay and take the next row's first tile under way (backward 106 us: registers);
-// reset flags a tile ahead (+6 us); a later row's first tile fetched into L2 by the warp before (no gain, or 2%).
+// Figures here and in gated_math.cuh and gated_launch.cuh: us of replayed graphs under a steady load (a cold call is up to
+// 5% faster where the power bounds the clock, a few us slower where it is short), bf16 with the output gate unless said,
+// every channel near (decay_of), the backward with the forward's checkpoints.  From box to box they differ by 3%.
+//
+// What bounds it: the special-function unit (forward: 6 operations a step, three exponentials, a reciprocal root, two
+// reciprocals; 71 to 76% of its peak) and issue (about 31 instructions a step forward, 65 backward, packed fp32 pairs
+// throughout, and some 300 and 400 a row; 50 to 66%) beside the bytes.  32768 steps of 5120 channels: 331 us, 77% of the copy
+// rate; 2048 steps of 8 x 1536 channels, forward and backward, 151 us (71%), with resets 164 (66%), fp32 252 (85%).
+// Channels beyond the near ones cost an exponential and a root more: 384 us instead of 343 for the former on one box, 164
+// instead of 155 for the second.  What was slower on earlier forms: the forward's operands through the backward's ring
+// (5% and more); warps that stay and take the next row's first tile under way (registers); reset flags a tile ahead
+// (3%); a later row's first tile fetched into L2 by the warp before (no gain, or 2%).
 #pragma once
 
 #include <type_traits>
@@ -44,8 +49,8 @@ constexpr int kMaxSplit = 8;    // warps of a block with SPLIT (two such blocks 
 constexpr int kMaxParts = 32;   // warps that share a row
 constexpr int kMaxCluster = 8;  // blocks that share a row
 // Blocks per SM that the registers are held to, so 128 registers, or 168 for the fp32 backward (3 x 1001 x 2047
-// forward and backward: 77 us with 3, 81 with 4).  More blocks spill: 5 took 432 us against 313 (forward, 5120 x
-// 32768), 147 against 111 (backward, 8 x 1536 x 2048).
+// forward and backward: 72 us with 3, 78 with 4).  More blocks spill: 5 took 384 us against 331 (forward, 5120 x
+// 32768), 116 against 96 (backward, 8 x 1536 x 2048).
 constexpr int kFwdBlocks = 4;
 template <typename IO> constexpr int kBwdBlocks = sizeof(IO) == 2 ? 4 : 3;
 

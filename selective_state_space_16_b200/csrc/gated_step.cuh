@@ -9,9 +9,10 @@
 namespace ssm {
 
 constexpr int kStepThreads = 128;
-// Resident blocks per SM (80 registers), which is also how many a launch has at most.  bf16 with the gate, graph
-// of 60 steps: 256 x 5120 6.1 us and 2048 x 5120 36 us (75% of the copy rate), with 8 blocks 6.2 and 34 but
-// fp32 512 x 8192 19.1 instead of 18.8 (spills), with 10 9.1 and 65; one row per block 7.2 and 69.
+// Resident blocks per SM (80 registers), which is also how many a launch has at most.  With the gate, graph of 60
+// steps: bf16 256 x 5120 6.5 us and 2048 x 5120 36.8 us (74% of the copy rate), with 8 blocks 6.6 and 36.4 but fp32 512 x
+// 8192 28.9 instead of 20.9 (spills), with 10 9.2 and 65.6; one row per block 9.0 and 89.9.  Channels that are not near
+// cost 2% (2048 x 5120), one in a warp's 128 as much as all.
 constexpr int kStepBlocks = 6;
 constexpr int kStepChannels = 4;  // per thread
 
