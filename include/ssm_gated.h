@@ -15,11 +15,11 @@
  * Conventions: those of ssm_scan.h (device pointers owned by the caller, no device memory
  * allocated, calls asynchronous on `stream`, status codes), and:
  *   - x, r, i, z, y and their gradients have io_dtype elements (fp32 or bf16), shape (batch, dim,
- *     seqlen) with consecutive steps next to each other; the batch and channel strides are given
- *     (in elements; those of an input may be zero or negative), so that slices of a wider tensor, such as the three parts of one
- *     projection's output, are taken as they are.  Any alignment of the elements' own size.  What lies
- *     between an operand's first and last row has to be readable memory: a few elements beside a row may
- *     be read with it (and are never used).
+ *     seqlen) with consecutive steps next to each other; the batch and channel strides are given (in
+ *     elements; those of an input may be zero or negative), so that slices of a wider tensor, such
+ *     as the three parts of one projection's output, are taken as they are.  Any alignment of the
+ *     elements' own size.  What lies between an operand's first and last row has to be readable
+ *     memory: a few elements beside a row may be read with it (and are never used).
  *   - lam, r_bias, i_bias, their gradients and every state are fp32 and dense; arithmetic is fp32.
  *   - lengths  NULL, or int32 (batch) on the device: row b has lengths[b] steps (values outside
  *     0 .. seqlen are taken as the nearest of the two).  What lies behind them is not read for any
